@@ -108,6 +108,7 @@ typedef enum gq_scale_mode {
 #define GQ_STATUS_NONFINITE 0x1  /* a NaN or +-inf in the tensor */
 #define GQ_STATUS_RANGE     0x2  /* binary16(c / qmax) overflowed to inf */
 #define GQ_STATUS_TIMEOUT   0x4  /* a bounded wait on the device gave up */
+#define GQ_STATUS_OFFSETS   0x8  /* gq_gemm_grouped: row offsets not ascending within the batch */
 
 /* Kinds returned by gq_plan_kind. */
 #define GQ_KIND_RAW  0  /* not floating point: stored as is */
@@ -437,6 +438,151 @@ GQ_API gq_status gq_gemm_fakequant(const void* d_x, int64_t M, int64_t K, int64_
                                    int32_t w_dtype, int64_t ldw, const float* d_clip, int qbits,
                                    gq_scale_mode mode, int64_t N, float* d_y, int64_t ldy, int32_t* d_status,
                                    cudaStream_t stream);
+
+/*
+ * The layer product with its epilogue, over weights laid out in tiles:
+ *   Z[m, n] = s[n] * sum_k X[m, k] * q[n, k] + bias[n]
+ *   Y[m, n] = act(Z[m, n]) + residual[m, n]
+ * with q the int6 / int8 codes and s[n] = (float)scale_f16[n] of an export per
+ * row, i.e. the weight is exactly the binary32 w_hat of gq_dequant (q * s fits
+ * binary32).  The codes go to the tensor cores as bf16 integers (exact), the
+ * sum is binary32 in the tensor cores' order, and scale, bias, activation and
+ * residual are binary32 steps on it; Y is rounded once to its type.
+ *
+ * gq_tile_weight lays a weight out once, after the export or at load: rows in
+ * tiles of 128, columns in blocks of 64 (both padded with code 0), a block of
+ * a tile contiguous as [16-byte chunk][row][16 bytes], the bits of an int6
+ * code placed so that two codes leave a word with one mask.  E weights of one
+ * shape (experts) lie one after the other: d_packed [E, N, packed row bytes]
+ * to d_tiles [E, gq_tile_bytes(N, K, qbits)].  d_packed has any alignment,
+ * d_tiles 16 bytes.  gq_tile_bytes is -1 for bad arguments.
+ *
+ * gq_gemm_epilogue arguments:
+ *   d_x      bf16 [M, ldx], 16-byte aligned, ldx % 8 == 0; any K, any M
+ *   d_tiles  as gq_tile_weight wrote them for [N, K], 16-byte aligned
+ *   d_scale_f16 [N] binary16 bit patterns, 2-byte aligned
+ *   epi      host struct, read during the call; NULL: Y = Z without bias, binary32.
+ *            bias: nullable, [N] of bias_dtype; residual: nullable, [M, ldr]
+ *            of residual_dtype, ldr >= N, may be Y itself (same pointer, type
+ *            and pitch); act: a gq_act; y_dtype: GQ_F32 or GQ_BF16
+ *   d_y      [M, ldy] of y_dtype, ldy >= N; columns N .. ldy - 1 are untouched
+ *   d_status nullable: cleared, then GQ_STATUS_TIMEOUT if a bounded wait on the
+ *            device gave up (Y is then not valid)
+ * Element pointers are aligned to their element size.  K = 0 gives Y =
+ * act(bias) + residual.  No workspace; Y is the same bits on every call with
+ * the same arguments (no atomics: a K range split over blocks is summed in a
+ * fixed order).  |Z - exact| <= (K/8 + 32) * 2^-24 * sum_k |X * W| plus one
+ * binary32 rounding for the scale and one for the bias.
+ * NaN and infinities of X, bias and residual propagate as in those formulas
+ * (relu(NaN) = NaN).
+ *
+ * gq_gemm_grouped is the same product with one weight per group of rows (the
+ * experts of a mixture, their rows sorted by expert): rows d_offsets[e] .. 
+ * d_offsets[e + 1] - 1 of X, residual and Y belong to expert e and use its
+ * tiles, scale [E, N] and bias [E, N].  d_offsets is device int32 [E + 1],
+ * non-decreasing in [0, M]; experts may have no row, and rows outside
+ * [d_offsets[0], d_offsets[E]) are not written (a padded batch).  An offset
+ * that decreases or lies outside [0, M] sets GQ_STATUS_OFFSETS and Y is then
+ * unspecified within its M rows.  E <= 65535.
+ * Source: the layers that consume the fake-quant weights, with the MLPs'
+ * ReLU^2 and LeakyReLU^2 (slope 0.5) of the pages; PR #69, PR #1202, PR #1495.
+ */
+typedef enum gq_act {
+    GQ_ACT_NONE = 0,
+    GQ_ACT_RELU = 1,
+    GQ_ACT_RELU2 = 2,         /* relu(z)^2 */
+    GQ_ACT_LEAKY_RELU2 = 3,   /* (z > 0 ? z : z / 2)^2 */
+    GQ_ACT_SILU = 4,          /* z / (1 + exp(-z)) */
+    GQ_ACT_GELU = 5,          /* z * Phi(z), by erf */
+    GQ_ACT_GELU_TANH = 6      /* its tanh form */
+} gq_act;
+
+typedef struct gq_epilogue {
+    const void* bias;
+    const void* residual;
+    int64_t ldr;
+    int32_t bias_dtype;
+    int32_t residual_dtype;
+    int32_t act;
+    int32_t y_dtype;
+} gq_epilogue;
+
+GQ_API int64_t gq_tile_bytes(int64_t N, int64_t K, int qbits);
+GQ_API gq_status gq_tile_weight(const uint8_t* d_packed, int64_t E, int64_t N, int64_t K, int qbits,
+                                uint8_t* d_tiles, cudaStream_t stream);
+GQ_API gq_status gq_gemm_epilogue(const void* d_x, int64_t M, int64_t K, int64_t ldx, const uint8_t* d_tiles,
+                                  const uint16_t* d_scale_f16, int qbits, int64_t N, const gq_epilogue* epi,
+                                  void* d_y, int64_t ldy, int32_t* d_status, cudaStream_t stream);
+GQ_API gq_status gq_gemm_grouped(const void* d_x, int64_t M, int64_t K, int64_t ldx, const int32_t* d_offsets,
+                                 int64_t E, const uint8_t* d_tiles, const uint16_t* d_scale_f16, int qbits,
+                                 int64_t N, const gq_epilogue* epi, void* d_y, int64_t ldy, int32_t* d_status,
+                                 cudaStream_t stream);
+
+/*
+ * One AdamW step (decoupled weight decay) of n tensors, in place:
+ *   g  = RN(g * grad_scale)                          (only where d_grad_scale is given)
+ *   m' = RN(RN(b1 * m) + RN(RN(1 - b1) * g)),  v' = RN(RN(b2 * v) + RN(RN(1 - b2) * RN(g * g)))
+ *   d  = RN(RN(sqrt(v') * RN(1 / sqrt(1 - b2^t))) + eps)
+ *   p' = RN(RN(p * RN(1 - lr * wd)) - RN(RN(m' / d) * RN(lr / (1 - b1^t))))
+ * in binary32 (the scalars in binary64, each rounded once; products such as
+ * lr * wd are in binary64); a bf16 weight is widened exactly and p' rounded
+ * to nearest even bf16.  Every output is bit-exact to that definition.
+ *
+ * States: binary32 m and v (state_bits 32), or 8 bits each with binary32
+ * scales per block of 256 consecutive elements (state_bits 8):
+ *   m = RN(qm * sm), qm int8 in [-127, 127];  v = RN(RN(qv^2)^2 * sv), qv uint8
+ * (a fourth power: v spans nine decades of a block, the codes densest
+ * where the block's large values lie).  New codes, with a = max |m'| (max v')
+ * of the block and f(q) = RN((q^2)^2):
+ *   sm = RN(a * RN(1 / 127)), x = RN(m' * RN(127 / a)), qm = clamp(floor(RN(x + u1)), -127, 127)
+ *   sv = RN(a * RN(1 / 255^4)), x = RN(v' * RN(255^4 / a)), q0 = the largest q <= 254 with f(q) <= x,
+ *   qv = q0 + (RN(u2 * RN(f(q0 + 1) - f(q0))) < RN(x - f(q0))), and 1 where that is 0 but x > 0;
+ *   a < 2^-80 gives scale 0 and codes 0.
+ * u1, u2 are 16 random bits each (k * 2^-16) from a hash of the element's
+ * index, the tensor's place in the batch, the step and the seed: rounding is
+ * unbiased, so that changes of a state smaller than a code's step are not
+ * lost, and reproducible.
+ *
+ * t[i]: p (fp32 / bf16), g (fp32 / bf16), m, v dense arrays of numel elements;
+ * m_scale, v_scale [ceil(numel / 256)] for 8-bit states, else NULL; p_copy
+ * nullable: bf16 copy of p' (the model's weights when p is the fp32 master).
+ * Pointers are aligned to their element size; 16-byte aligned ones take the
+ * vector path.  numel 0 is a no-op.  h: host struct.
+ * d_step, d_lr (nullable, device): read by the kernel instead of h->step and
+ * h->lr, so that a captured step can be replayed while both move on.
+ * d_grad_scale nullable, device binary32 (loss unscaling, clipping).
+ * A non-finite gradient reaches p, m and v as the formulas say (32-bit); in an
+ * 8-bit block whose m' or v' has a NaN or an infinity the new codes and
+ * scales of that block are unspecified.
+ * Asynchronous on `stream`; one launch per 200 tensors.
+ * Source: AdamW with decoupled weight decay (PR #69, PR #1414).
+ */
+typedef struct gq_adamw_tensor {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    uint16_t* p_copy;
+    int64_t numel;
+    int32_t p_dtype;
+    int32_t g_dtype;
+    int32_t state_bits;       /* 32 or 8 */
+    int32_t reserved;         /* must be 0 */
+    double weight_decay;
+} gq_adamw_tensor;
+
+typedef struct gq_adamw_hyper {
+    double lr, beta1, beta2, eps;
+    int64_t step;             /* t >= 1: the number of the step being taken */
+    uint64_t seed;            /* 8-bit states: of the rounding's random bits (low 32 bits used) */
+    const int64_t* d_step;
+    const float* d_lr;
+    const float* d_grad_scale;
+} gq_adamw_hyper;
+
+GQ_API gq_status gq_adamw_step(const gq_adamw_tensor* t, int n, const gq_adamw_hyper* h, cudaStream_t stream);
 
 /* Device workspace bytes a batch needs (0 when it has no per-tensor group). */
 GQ_API size_t gq_workspace_size(const gq_tensor* t, int n);

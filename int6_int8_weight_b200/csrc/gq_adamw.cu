@@ -1,0 +1,100 @@
+// gq_adamw.cu -- host side of gq_adamw_step (include/gq.h).
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "gq_adamw.cuh"
+#include "gq_host.h"
+
+namespace {
+
+using namespace gq;
+
+static_assert(sizeof(gq_adamw_tensor) == 88 && sizeof(gq_adamw_hyper) == 72,
+              "the layouts are part of the ABI (the Python binding mirrors them)");
+static_assert(sizeof(AdamParams) <= 32764, "kernel parameters end at 32764 bytes");
+
+gq_status check_adamw(const gq_adamw_tensor& t) {
+    if (t.reserved != 0 || t.numel < 0) return GQ_ERR_INVALID_ARG;
+    if ((t.p_dtype != GQ_F32 && t.p_dtype != GQ_BF16) || (t.g_dtype != GQ_F32 && t.g_dtype != GQ_BF16))
+        return GQ_ERR_INVALID_ARG;
+    if (t.state_bits != 32 && t.state_bits != 8) return GQ_ERR_INVALID_ARG;
+    if (!std::isfinite(t.weight_decay)) return GQ_ERR_INVALID_ARG;
+    if (t.numel > INT64_MAX / 16) return GQ_ERR_INVALID_ARG;
+    if (t.numel == 0) return GQ_OK;
+    if (!t.p || !t.g || !t.m || !t.v) return GQ_ERR_INVALID_ARG;
+    if (t.state_bits == 8 ? (!t.m_scale || !t.v_scale) : (t.m_scale || t.v_scale)) return GQ_ERR_INVALID_ARG;
+    const size_t ps = t.p_dtype == GQ_F32 ? 4 : 2, gs = t.g_dtype == GQ_F32 ? 4 : 2, ss = t.state_bits / 8;
+    if (!aligned(t.p, ps) || !aligned(t.g, gs) || !aligned(t.m, ss) || !aligned(t.v, ss) ||
+        (t.p_copy && !aligned(t.p_copy, 2)) || (t.m_scale && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
+        return GQ_ERR_MISALIGNED;
+    return GQ_OK;
+}
+
+}  // namespace
+
+extern "C" gq_status gq_adamw_step(const gq_adamw_tensor* t, int n, const gq_adamw_hyper* h, cudaStream_t stream) {
+    if (n < 0 || (n > 0 && !t) || !h) return GQ_ERR_INVALID_ARG;
+    if (!(h->beta1 >= 0.0 && h->beta1 < 1.0) || !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps >= 0.0) ||
+        !std::isfinite(h->eps) || !std::isfinite(h->lr) || (!h->d_step && h->step < 1))
+        return GQ_ERR_INVALID_ARG;
+    if ((h->d_step && !aligned(h->d_step, 8)) || (h->d_lr && !aligned(h->d_lr, 4)) ||
+        (h->d_grad_scale && !aligned(h->d_grad_scale, 4)))
+        return GQ_ERR_MISALIGNED;
+    for (int i = 0; i < n; ++i) {
+        const gq_status st = check_adamw(t[i]);
+        if (st != GQ_OK) return st;
+    }
+    AdamParams P;
+    const int64_t step = h->d_step ? 1 : h->step;
+    P.lr = h->lr;
+    P.beta1 = h->beta1;
+    P.beta2 = h->beta2;
+    P.bias1 = 1.0 - std::pow(h->beta1, (double)step);
+    P.b1 = (float)h->beta1;
+    P.c1 = (float)(1.0 - h->beta1);
+    P.b2 = (float)h->beta2;
+    P.c2 = (float)(1.0 - h->beta2);
+    P.eps = (float)h->eps;
+    P.inv_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h->beta2, (double)step)));
+    P.step_size = (float)(h->lr / P.bias1);
+    P.key_step = (uint32_t)step * kAdamStepMul;
+    P.d_step = h->d_step;
+    P.d_lr = h->d_lr;
+    P.d_grad_scale = h->d_grad_scale;
+    for (int base = 0; base < n; base += kAdamDesc) {
+        const int nd = std::min(kAdamDesc, n - base);
+        int64_t items = 0;
+        P.ndesc = 0;
+        for (int i = 0; i < nd; ++i) {
+            const gq_adamw_tensor& T = t[base + i];
+            if (T.numel == 0) continue;
+            AdamDesc& D = P.d[P.ndesc];
+            D.p = T.p;
+            D.g = T.g;
+            D.m = T.m;
+            D.v = T.v;
+            D.ms = T.m_scale;
+            D.vs = T.v_scale;
+            D.copy = T.p_copy;
+            D.numel = T.numel;
+            D.wd = T.weight_decay;
+            D.decay = (float)(1.0 - h->lr * T.weight_decay);
+            D.key = (uint32_t)h->seed + (uint32_t)(base + i) * kAdamTensorMul;
+            const size_t sa = T.state_bits == 8 ? 8 : 16;
+            const bool vec = aligned(T.p, 16) && aligned(T.g, 16) && aligned(T.m, sa) && aligned(T.v, sa) &&
+                             (!T.p_copy || aligned(T.p_copy, 16));
+            D.flags = (T.p_dtype == GQ_BF16 ? kAdamPBf16 : 0) | (T.g_dtype == GQ_BF16 ? kAdamGBf16 : 0) |
+                      (T.state_bits == 8 ? kAdamState8 : 0) | (vec ? kAdamVec : 0);
+            D.pad = 0;
+            P.start[P.ndesc++] = items;
+            items += (T.numel + kAdamItem - 1) / kAdamItem;
+        }
+        P.start[P.ndesc] = items;
+        if (items == 0) continue;
+        const int64_t blocks = std::min<int64_t>(items, (int64_t)sm_count() * 32);
+        adamw_kernel<<<(unsigned)blocks, kAdamThreads, 0, stream>>>(P);
+        if (launch_status() != GQ_OK) return GQ_ERR_CUDA;
+    }
+    return GQ_OK;
+}

@@ -12,7 +12,7 @@
 #include <vector>
 
 #include "gq.h"
-#include <cudaTypedefs.h>
+#include "gq_host.h"
 
 #include "gq_aux_kernels.cuh"
 #include "gq_gemm.cuh"
@@ -26,8 +26,11 @@ namespace {
 using namespace gq;
 
 constexpr size_t kWsSlot = 8448;      // 2048 x u32 histogram + 16 x u32 state, 256-aligned
-constexpr int kMaxDevices = 64;
 std::atomic<int> g_sm_count[kMaxDevices];
+
+}  // namespace
+
+namespace gq {
 
 int sm_count() {
     int dev = 0;
@@ -43,6 +46,10 @@ int sm_count() {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+}  // namespace gq
+
+namespace {
+
 int64_t k_from_p(int64_t n, double p) {
     double prod = p * (double)n;
     double up = std::ceil(prod);
@@ -52,13 +59,17 @@ int64_t k_from_p(int64_t n, double p) {
     return k;
 }
 
-int64_t packed_row_bytes(int64_t cols, int qbits) {
+}  // namespace
+
+int64_t gq::packed_row_bytes(int64_t cols, int qbits) {
     if (cols < 0) return -1;
     if (qbits == 6) return 3 * ((cols + 3) / 4);
     if (qbits == 8) return cols;
     if (qbits == 16) return 2 * cols;
     return -1;
 }
+
+namespace {
 
 enum class Op { Select, FakeQuant, Export, Average };
 
@@ -144,14 +155,18 @@ size_t workspace_size(const gq_tensor* t, int n, bool cand = true) {
 
 thread_local int g_last_cuda_error = 0;
 
+}  // namespace
+
 // GQ_OK, or GQ_ERR_CUDA after recording the CUDA error for gq_last_cuda_error.
-gq_status cuda_status(cudaError_t e) {
+gq_status gq::cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return GQ_OK;
     g_last_cuda_error = (int)e;
     return GQ_ERR_CUDA;
 }
 
-gq_status launch_status() { return cuda_status(cudaGetLastError()); }
+gq_status gq::launch_status() { return cuda_status(cudaGetLastError()); }
+
+namespace {
 
 // Per-tensor radix select for every per-tensor descriptor (three passes).
 gq_status run_per_tensor_select(const std::vector<SelDesc>& sel, cudaStream_t stream) {
@@ -496,9 +511,11 @@ std::atomic<void*> g_encode_tiled{nullptr};
 std::atomic<int> g_gemm_smem_set[2][kMaxDevices];
 std::atomic<int> g_dec_smem_set[2][kMaxDevices];
 
+}  // namespace
+
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no
 // link-time dependency on the driver library).
-PFN_cuTensorMapEncodeTiled encode_tiled() {
+PFN_cuTensorMapEncodeTiled gq::encode_tiled() {
     void* f = g_encode_tiled.load(std::memory_order_acquire);
     if (!f) {
         cudaDriverEntryPointQueryResult q{};
@@ -509,6 +526,8 @@ PFN_cuTensorMapEncodeTiled encode_tiled() {
     }
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled>(f);
 }
+
+namespace {
 
 // Scratch of gq_export_pack_noalloc: a fixed device array that every call on
 // a device shares, for callers that cannot hand the library any device memory.

@@ -10,8 +10,10 @@ the same arguments as the C entry points (pointers as ints, the stream as a
 
 High level: ``fakequant`` / ``export_pack`` / ``row_clip_select`` take torch
 tensors, allocate the requested outputs and return them; ``FakeQuantSTE`` is
-the autograd function of the straight-through estimator; ``dequant`` and
-``ste_bwd`` wrap the remaining calls; ``plan_kind`` / ``export_state_dict``
+the autograd function of the straight-through estimator; ``tile_weight``,
+``gemm_epilogue`` and ``gemm_grouped`` run layers over the exported codes;
+``adamw_step`` is the optimizer's step; ``dequant`` and ``ste_bwd`` wrap the
+remaining calls; ``plan_kind`` / ``export_state_dict``
 apply the mixed-bit export plan.
 """
 from __future__ import annotations
@@ -29,7 +31,9 @@ GQ_OK = 0
 GQ_F32, GQ_BF16 = 0, 1
 GQ_PER_ROW, GQ_PER_TENSOR = 0, 1
 GQ_SCALE_F32, GQ_SCALE_F16 = 0, 1
-GQ_STATUS_NONFINITE, GQ_STATUS_RANGE, GQ_STATUS_TIMEOUT = 1, 2, 4
+GQ_STATUS_NONFINITE, GQ_STATUS_RANGE, GQ_STATUS_TIMEOUT, GQ_STATUS_OFFSETS = 1, 2, 4, 8
+ACTS = {"none": 0, "relu": 1, "relu2": 2, "leaky_relu2": 3, "silu": 4, "gelu": 5, "gelu_tanh": 6}
+ADAMW_BLOCK = 256                # elements that share an 8-bit state's scale
 GQ_AVG_MEAN, GQ_AVG_EMA = 0, 1
 GQ_KIND_RAW, GQ_KIND_FP16, GQ_KIND_INT8, GQ_KIND_INT6 = 0, 1, 2, 3
 KIND_NAMES = {GQ_KIND_RAW: "raw", GQ_KIND_FP16: "fp16", GQ_KIND_INT8: "int8", GQ_KIND_INT6: "int6"}
@@ -42,7 +46,8 @@ EXPORTED = ("gq_row_clip_select", "gq_fakequant_fwd", "gq_fakequant_average", "g
             "gq_export_pack_noalloc", "gq_dequant", "gq_gemm_dequant", "gq_workspace_size", "gq_packed_row_bytes", "gq_k_from_p",
             "gq_plan_kind", "gq_status_string", "gq_last_cuda_error", "gq_last_cuda_error_string",
             "gq_test_arm_wait_expiry", "gq_gptq_quantize", "gq_gptq_hessian", "gq_gptq_workspace_size",
-            "gq_gemm_fakequant", "gq_gptq_quantize_batch", "gq_gptq_batch_workspace_size")
+            "gq_gemm_fakequant", "gq_gptq_quantize_batch", "gq_gptq_batch_workspace_size", "gq_tile_bytes",
+            "gq_tile_weight", "gq_gemm_epilogue", "gq_gemm_grouped", "gq_adamw_step")
 
 
 class GQError(RuntimeError):
@@ -65,6 +70,24 @@ class GQTensor(C.Structure):
 
 class GQAvg(C.Structure):
     _fields_ = [("avg", C.c_void_p), ("kind", C.c_int32), ("decay", C.c_float), ("count", C.c_int64)]
+
+
+class GQEpilogue(C.Structure):
+    _fields_ = [("bias", C.c_void_p), ("residual", C.c_void_p), ("ldr", C.c_int64), ("bias_dtype", C.c_int32),
+                ("residual_dtype", C.c_int32), ("act", C.c_int32), ("y_dtype", C.c_int32)]
+
+
+class GQAdamWTensor(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("m_scale", C.c_void_p), ("v_scale", C.c_void_p), ("p_copy", C.c_void_p), ("numel", C.c_int64),
+                ("p_dtype", C.c_int32), ("g_dtype", C.c_int32), ("state_bits", C.c_int32), ("reserved", C.c_int32),
+                ("weight_decay", C.c_double)]
+
+
+class GQAdamWHyper(C.Structure):
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double),
+                ("step", C.c_int64), ("seed", C.c_uint64), ("d_step", C.c_void_p), ("d_lr", C.c_void_p),
+                ("d_grad_scale", C.c_void_p)]
 
 
 def _load() -> C.CDLL:
@@ -98,6 +121,15 @@ def _load() -> C.CDLL:
     L.gq_gptq_hessian.restype = i32
     L.gq_gptq_workspace_size.argtypes = [i64, i64]
     L.gq_gptq_workspace_size.restype = sz
+    L.gq_tile_bytes.argtypes = [i64, i64, i32]
+    L.gq_tile_bytes.restype = i64
+    L.gq_tile_weight.argtypes = [vp, i64, i64, i64, i32, vp, vp]
+    L.gq_gemm_epilogue.argtypes = [vp, i64, i64, i64, vp, vp, i32, i64, C.POINTER(GQEpilogue), vp, i64, vp, vp]
+    L.gq_gemm_grouped.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp, i32, i64, C.POINTER(GQEpilogue), vp, i64, vp,
+                                  vp]
+    L.gq_adamw_step.argtypes = [C.POINTER(GQAdamWTensor), i32, C.POINTER(GQAdamWHyper), vp]
+    for f in ("gq_tile_weight", "gq_gemm_epilogue", "gq_gemm_grouped", "gq_adamw_step"):
+        getattr(L, f).restype = i32
     L.gq_test_arm_wait_expiry.argtypes = [i64, C.c_uint64]
     L.gq_test_arm_wait_expiry.restype = i32
     L.gq_workspace_size.argtypes = [T, i32]
@@ -507,6 +539,173 @@ def gemm_fakequant(x: torch.Tensor, w: torch.Tensor, clip: torch.Tensor, qbits: 
                                  clip.data_ptr(), qbits, mode, N, y.data_ptr(), y.stride(0), None,
                                  _stream(stream)), "gq_gemm_fakequant")
     return y
+
+
+def _on(device: torch.device, stream, fn, *args) -> int:
+    """``fn(*args, stream)`` with ``device`` current; its current stream where ``stream`` is None."""
+    if device.type != "cuda":
+        raise ValueError("libgq takes CUDA tensors")
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(stream))
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"every tensor of a call lies on one device ({device}, {t.device})")
+
+
+def tile_weight(packed: torch.Tensor, K: int, qbits: int, stream=None) -> torch.Tensor:
+    """The tile layout of exported codes (gq_tile_weight), made once after the
+    export or at load: ``packed`` uint8 [N, packed row bytes] (or [E, N, packed
+    row bytes], one weight per expert) of K columns -> uint8 [bytes] ([E, bytes]),
+    the weight argument of ``gemm_epilogue`` (``gemm_grouped``)."""
+    if packed.dtype != torch.uint8 or packed.dim() not in (2, 3) or not packed.is_contiguous():
+        raise ValueError("packed must be a contiguous uint8 [N, row bytes] or [E, N, row bytes] tensor")
+    if qbits not in (6, 8) or packed.shape[-1] != gq_packed_row_bytes(K, qbits):
+        raise ValueError(f"packed rows of {K} columns hold {gq_packed_row_bytes(K, qbits)} bytes, "
+                         f"got {packed.shape[-1]}")
+    E, N = (1, packed.shape[0]) if packed.dim() == 2 else packed.shape[:2]
+    nbytes = LIB.gq_tile_bytes(N, K, qbits)
+    tiles = torch.empty((nbytes,) if packed.dim() == 2 else (E, nbytes), dtype=torch.uint8, device=packed.device)
+    _check(_on(packed.device, stream, LIB.gq_tile_weight, packed.data_ptr(), E, N, K, qbits, tiles.data_ptr()),
+           "gq_tile_weight")
+    return tiles
+
+
+def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, out_dtype, stream, check_status):
+    """Argument checks and the call shared by gemm_epilogue and gemm_grouped."""
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or (x.shape[0] and x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError("x must be a bf16 [M, K] tensor with contiguous rows")
+    M, K = x.shape
+    lead = scale.shape[:-1]
+    if scale.dtype != torch.float16 or not scale.is_contiguous() or scale.dim() != (2 if offsets is not None else 1):
+        raise ValueError("scale_f16 must be a contiguous fp16 tensor, [N] (grouped: [E, N])")
+    N = scale.shape[-1]
+    if tiles.dtype != torch.uint8 or not tiles.is_contiguous() or tiles.shape[:-1] != lead \
+            or tiles.shape[-1] != LIB.gq_tile_bytes(N, K, qbits):
+        raise ValueError("tiles must be what tile_weight gives for these N, K and qbits")
+    if act not in ACTS:
+        raise ValueError(f"act is one of {', '.join(ACTS)}")
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=x.device)
+    elif y.shape != (M, N) or (M and y.stride(1) != 1 and N > 1) or (out_dtype is not None and y.dtype != out_dtype):
+        raise ValueError("y must be [M, N] with contiguous rows and of out_dtype where that is given")
+    e = GQEpilogue(act=ACTS[act], y_dtype=_dtype_code(y))
+    if bias is not None:
+        if bias.shape != scale.shape or not bias.is_contiguous():
+            raise ValueError("bias must be contiguous, of the shape of scale_f16")
+        e.bias, e.bias_dtype = bias.data_ptr(), _dtype_code(bias)
+    if residual is not None:
+        if residual.shape != (M, N) or (M and residual.stride(1) != 1 and N > 1):
+            raise ValueError("residual must be [M, N] with contiguous rows")
+        e.residual, e.residual_dtype, e.ldr = residual.data_ptr(), _dtype_code(residual), max(residual.stride(0), N)
+    _same_device(x.device, offsets, tiles, scale, bias, residual, y)
+    group = () if offsets is None else (offsets.data_ptr(), scale.shape[0])
+    st = torch.empty(1, dtype=torch.int32, device=x.device) if check_status else None
+    _check(_on(x.device, stream, fn, x.data_ptr(), M, K, max(x.stride(0), K) if M > 1 else -(-K // 8) * 8, *group,
+               tiles.data_ptr(), scale.data_ptr(), qbits, N, C.byref(e), y.data_ptr(),
+               max(y.stride(0), N) if M > 1 else N, _ptr(st) or None), where)
+    if check_status and (v := int(st.item())):
+        raise GQError(0, where, f"device status {v:#x}")
+    return y
+
+
+def gemm_epilogue(x: torch.Tensor, tiles: torch.Tensor, scale_f16: torch.Tensor, qbits: int,
+                  bias: torch.Tensor | None = None, act: str = "none", residual: torch.Tensor | None = None,
+                  y: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, stream=None,
+                  check_status: bool = False) -> torch.Tensor:
+    """Y = act(X @ W^T + bias) + residual with W[n, k] = q[n, k] * s[n] from the
+    tiles of ``tile_weight`` and the export's binary16 row scales, in one kernel
+    (gq_gemm_epilogue).  ``x`` is bf16 [M, K], rows contiguous, starting on 16
+    bytes, with a pitch that is a multiple of 8; ``bias`` fp32 / bf16 [N];
+    ``residual`` fp32 / bf16 [M, N], may be ``y``; Y is [M, N], bf16 unless
+    ``y`` or ``out_dtype`` says fp32.  ``check_status`` waits for the call and
+    raises if it gave up."""
+    return _layer("gq_gemm_epilogue", LIB.gq_gemm_epilogue, x, None, tiles, scale_f16, qbits, bias, act, residual, y,
+                  out_dtype, stream, check_status)
+
+
+def gemm_grouped(x: torch.Tensor, offsets: torch.Tensor, tiles: torch.Tensor, scale_f16: torch.Tensor, qbits: int,
+                 bias: torch.Tensor | None = None, act: str = "none", residual: torch.Tensor | None = None,
+                 y: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, stream=None,
+                 check_status: bool = False) -> torch.Tensor:
+    """``gemm_epilogue`` with one weight per group of rows (gq_gemm_grouped):
+    rows offsets[e] .. offsets[e + 1] - 1 of ``x``, sorted by expert, use
+    tiles[e], scale_f16[e] and bias[e].  ``offsets`` is int32 [E + 1] on the
+    device; experts may be empty, and rows outside [offsets[0], offsets[E]) of
+    ``y`` stay as they were."""
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() \
+            or offsets.shape[0] != scale_f16.shape[0] + 1:
+        raise ValueError("offsets must be a contiguous int32 [E + 1] tensor")
+    return _layer("gq_gemm_grouped", LIB.gq_gemm_grouped, x, offsets, tiles, scale_f16, qbits, bias, act, residual, y,
+                  out_dtype, stream, check_status)
+
+
+def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
+               weight_decay=0.01, scales=None, copies=None, grad_scale: torch.Tensor | None = None, seed: int = 0,
+               stream=None) -> None:
+    """One AdamW step over lists of tensors, in place (gq_adamw_step).
+
+    ``params`` / ``grads`` fp32 or bf16; ``exp_avgs`` / ``exp_avg_sqs`` fp32, or
+    int8 / uint8 codes with ``scales`` = (lists of) their fp32 block scales
+    [ceil(numel / 256)] (all zeros at the start); ``copies`` bf16 copies of the
+    new weights (a list, entries may be None).  ``step`` (from 1) and ``lr`` are
+    numbers, or int64 / fp32 tensors on the device that a captured step reads
+    when it is replayed.  ``weight_decay``: one number or one per tensor.
+    ``grad_scale``: fp32 device tensor that multiplies every gradient.  ``seed``
+    is that of the 8-bit states' rounding."""
+    n = len(params)
+    if not (len(grads) == len(exp_avgs) == len(exp_avg_sqs) == n) or (copies is not None and len(copies) != n) \
+            or (scales is not None and (len(scales) != 2 or len(scales[0]) != n or len(scales[1]) != n)):
+        raise ValueError("params, grads, states, scales and copies are lists of one length")
+    if n == 0:
+        return
+    wds = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else weight_decay
+    if len(wds) != n:
+        raise ValueError("weight_decay is a number or one per tensor")
+    dev = params[0].device
+    arr = (GQAdamWTensor * n)()
+    for i, (p, g, m, v) in enumerate(zip(params, grads, exp_avgs, exp_avg_sqs)):
+        numel = p.numel()
+        bits = 32 if scales is None else 8
+        want = (torch.float32, torch.float32) if bits == 32 else (torch.int8, torch.uint8)
+        if (m.dtype, v.dtype) != want:
+            raise TypeError("states are fp32, or int8 / uint8 codes with scales")
+        if not (g.numel() == m.numel() == v.numel() == numel) \
+                or not (p.is_contiguous() and g.is_contiguous() and m.is_contiguous() and v.is_contiguous()):
+            raise ValueError("weights, gradients and states are contiguous and of one size")
+        if not (p.device == g.device == m.device == v.device == dev):
+            raise ValueError("every tensor of a call lies on one device")
+        t = arr[i]
+        t.p, t.g, t.m, t.v, t.numel = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), numel
+        t.p_dtype, t.g_dtype, t.state_bits, t.weight_decay = _dtype_code(p), _dtype_code(g), bits, wds[i]
+        if bits == 8:
+            ms, vs = scales[0][i], scales[1][i]
+            if ms.dtype != torch.float32 or vs.dtype != torch.float32 or not ms.is_contiguous() \
+                    or not vs.is_contiguous() or not (ms.numel() == vs.numel() == -(-numel // ADAMW_BLOCK)):
+                raise ValueError("scales are contiguous fp32 tensors of ceil(numel / 256) elements")
+            _same_device(dev, ms, vs)
+            t.m_scale, t.v_scale = ms.data_ptr(), vs.data_ptr()
+        if copies is not None and copies[i] is not None:
+            c = copies[i]
+            if c.dtype != torch.bfloat16 or c.numel() != numel or not c.is_contiguous():
+                raise ValueError("copies are contiguous bf16 tensors of the weights' sizes")
+            _same_device(dev, c)
+            t.p_copy = c.data_ptr()
+    h = GQAdamWHyper(beta1=betas[0], beta2=betas[1], eps=eps, seed=seed & 0xFFFFFFFF)
+    for name, value, dtype in (("step", step, torch.int64), ("lr", lr, torch.float32),
+                               ("grad_scale", grad_scale, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            if value.dtype != dtype or value.numel() != 1:
+                raise ValueError(f"{name} on the device is one {dtype} element")
+            _same_device(dev, value)
+            setattr(h, "d_" + name, value.data_ptr())
+        elif value is not None:
+            setattr(h, name, value)
+    _check(_on(dev, stream, LIB.gq_adamw_step, arr, n, C.byref(h)), "gq_adamw_step")
 
 
 def ste_bwd(g_out: torch.Tensor, g_w: torch.Tensor | None = None, stream=None) -> torch.Tensor:
