@@ -1,6 +1,7 @@
 // gq_linear.cu -- host side of gq_tile_weight, gq_gemm_epilogue and
 // gq_gemm_grouped (include/gq.h): argument checks, launch planning, launches.
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "gq_host.h"
@@ -10,7 +11,59 @@ namespace {
 
 using namespace gq;
 
+constexpr int kLinSmem = 112 * 1024;     // a block's share of an SM that holds two
+
 static_assert(sizeof(gq_epilogue) == 40, "the layout is part of the ABI (the Python binding mirrors it)");
+
+// X [M, K] as a tensor map with a box of 64 columns x `rows` rows; zeros past the ends.
+bool map_x(CUtensorMap* map, const void* d_x, int64_t M, int64_t K, int64_t ldx, int rows) {
+    PFN_cuTensorMapEncodeTiled enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dim[2] = {(cuuint64_t)K, (cuuint64_t)M};
+    const cuuint64_t stride[1] = {(cuuint64_t)ldx * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kLinK, (cuuint32_t)rows};
+    const cuuint32_t step[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(d_x), dim, stride, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int QB, int NT>
+gq_status launch(LinParams& P, const void* d_x, int64_t K, int64_t ldx, cudaStream_t stream) {
+    using S = LinShape<QB, NT>;
+    static std::atomic<bool> set[kMaxDevices];
+    if (!map_x(&P.tmap_x, d_x, P.M, K, ldx, NT)) return GQ_ERR_UNSUPPORTED;
+    P.idesc = gemm_idesc(kLinRows, NT);
+    // token tiles: exact for one weight; for experts the most that any offsets can give
+    const int64_t tts = P.offsets ? P.M / NT + std::min<int64_t>(P.E, P.M) : (P.M + NT - 1) / NT;
+    const int64_t units = tts * P.rts;
+    int split = 1;
+    while (split < 8 && units * split * 2 <= 2 * (int64_t)sm_count() && P.kbs >= 4 * split) split *= 2;
+    if (units * split > INT32_MAX) return GQ_ERR_UNSUPPORTED;
+    P.split = split;
+    // two blocks to an SM
+    P.stages = std::min<int>(kLinMaxStages, (kLinSmem - S::smem(0)) / (int)S::stage);
+    const int smem = std::max(S::smem(P.stages), split > 1 ? S::smem(0) + NT * kLinRows * 4 : 0);
+    int dev = 0;
+    if (cuda_status(cudaGetDevice(&dev)) != GQ_OK) return GQ_ERR_CUDA;
+    if (dev >= kMaxDevices || !set[dev].load(std::memory_order_relaxed)) {
+        if (cuda_status(cudaFuncSetAttribute(linear_kernel<QB, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kLinSmem)) != GQ_OK)
+            return GQ_ERR_CUDA;
+        if (dev < kMaxDevices) set[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(units * split));
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {(unsigned)split, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    return cuda_status(cudaLaunchKernelEx(&cfg, linear_kernel<QB, NT>, static_cast<const LinParams&>(P)));
+}
 
 gq_status linear(const void* d_x, int64_t M, int64_t K, int64_t ldx, const int32_t* d_offsets, int64_t E,
                  const uint8_t* d_tiles, const uint16_t* d_scale_f16, int qbits, int64_t N, const gq_epilogue* epi,
@@ -41,24 +94,29 @@ gq_status linear(const void* d_x, int64_t M, int64_t K, int64_t ldx, const int32
     if (empty) return GQ_OK;
     LinParams P;
     std::memset(&P, 0, sizeof(P));
-    P.x = static_cast<const uint16_t*>(d_x);
     P.tiles = d_tiles;
     P.scale = d_scale_f16;
     P.offsets = d_offsets;
     P.status = d_status;
     P.M = M;
     P.N = N;
-    P.K = K;
-    P.ldx = ldx;
-    P.kbs = (K + kLinK - 1) / kLinK;
-    P.rts = (N + kLinRows - 1) / kLinRows;
     P.E = E;
+    P.kbs = (int32_t)((K + kLinK - 1) / kLinK);
+    P.rts = (int32_t)((N + kLinRows - 1) / kLinRows);
     P.epi = LinEpi{e.bias, e.residual, d_y, e.ldr, ldy, e.bias_dtype == GQ_BF16, e.residual_dtype == GQ_BF16,
                    e.y_dtype == GQ_BF16, e.act};
-    const dim3 grid((unsigned)P.rts, (unsigned)std::min<int64_t>((M + 7) / 8, 64), (unsigned)E);
-    if (qbits == 6) linear_kernel<6><<<grid, kLinRows, 0, stream>>>(P);
-    else linear_kernel<8><<<grid, kLinRows, 0, stream>>>(P);
-    return launch_status();
+    if (K == 0) {
+        linear_empty_kernel<<<(unsigned)std::min<int64_t>(M, 65535), 256, 0, stream>>>(P);
+        return launch_status();
+    }
+    // tokens of a tile: the rows an expert has on average, rounded up to 16 .. 128
+    const int64_t rows = (M + E - 1) / E;
+    const int nt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    if (qbits == 6)
+        return nt == 16 ? launch<6, 16>(P, d_x, K, ldx, stream) : nt == 32 ? launch<6, 32>(P, d_x, K, ldx, stream)
+             : nt == 64 ? launch<6, 64>(P, d_x, K, ldx, stream) : launch<6, 128>(P, d_x, K, ldx, stream);
+    return nt == 16 ? launch<8, 16>(P, d_x, K, ldx, stream) : nt == 32 ? launch<8, 32>(P, d_x, K, ldx, stream)
+         : nt == 64 ? launch<8, 64>(P, d_x, K, ldx, stream) : launch<8, 128>(P, d_x, K, ldx, stream);
 }
 
 }  // namespace

@@ -138,76 +138,367 @@ __device__ __forceinline__ void lin_finish(const LinEpi& E, float acc, float s, 
 }
 
 struct LinParams {
-    const uint16_t* x;
+    CUtensorMap tmap_x;          // X [M, K] bf16, box {64, tokens of a tile}, SWIZZLE_128B
     const uint8_t* tiles;
     const uint16_t* scale;
     const int32_t* offsets;      // [E + 1] or null (one weight)
     int32_t* status;
-    int64_t M, N, K, ldx, kbs, rts, E;
+    int64_t M, N, E;
+    int32_t kbs, rts;            // column blocks, row tiles of a weight
+    int32_t split;               // blocks (a cluster) that share a tile's column blocks
+    int32_t stages;              // ring depth
+    uint32_t idesc;
     LinEpi epi;
 };
 
-// The rows [a, b) of expert e within [0, M), and whether its offsets are right.
-__device__ __forceinline__ bool lin_rows(const int32_t* off, int64_t e, int64_t M, int64_t& a, int64_t& b) {
-    const int32_t p = off[e], q = off[e + 1];
-    a = max((int64_t)p, (int64_t)0);
-    b = min((int64_t)q, M);
-    return p >= 0 && q >= p && q <= M;
+// ------------------------------------------------------------- PTX glue --
+
+// Bulk copy of `bytes` (a multiple of 16) global -> this block's shared memory.
+__device__ __forceinline__ void lin_bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
-// The plainest form: one thread per row of a tile, 8 tokens at a time.
+__device__ __forceinline__ void lin_tmem_ld8(uint32_t taddr, float (&f)[8]) {
+    uint32_t v[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]);
+}
+
+// The binary32 at shared address `addr` of block `rank` of the cluster.
+__device__ __forceinline__ float lin_ld_peer(uint32_t addr, uint32_t rank) {
+    float f;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(f)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return f;
+}
+
+__device__ __forceinline__ void lin_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One weight row's 64 codes of a block (its 16-byte chunks lie 2048 bytes apart
+// at shared address `src`) into the 32 TMEM columns at `taddr` of this
+// thread's lane: column j holds k = 2j and 2j + 1 as bf16.
 template <int QB>
-__global__ void __launch_bounds__(kLinRows) linear_kernel(const __grid_constant__ LinParams P) {
-    __shared__ float xs[8][kLinK];
-    const int r = threadIdx.x;
-    const int64_t rt = blockIdx.x, e = blockIdx.z;
-    int64_t a = 0, b = P.M;
-    if (P.offsets && !lin_rows(P.offsets, e, P.M, a, b)) {
-        if (P.status && r == 0) atomicOr(reinterpret_cast<unsigned int*>(P.status), 8u);
-        return;
+__device__ __forceinline__ void lin_codes_to_tmem(uint32_t src, uint32_t taddr) {
+    constexpr int kChunks = QB == 6 ? 3 : 4;
+    uint32_t w[4 * kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                     : "r"(src + 16u * kLinRows * c)
+                     : "memory");
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t o[16];
+        if constexpr (QB == 6) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t t[8];
+                lin_codes6(w[6 * h + 3 * g], w[6 * h + 3 * g + 1], w[6 * h + 3 * g + 2], t);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[8 * g + j] = t[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) lin_codes8(w[8 * h + j], o[2 * j], o[2 * j + 1]);
+        }
+        g_tmem_st16(taddr + 16u * h, o);
     }
-    const int64_t n = rt * kLinRows + r;
-    const uint8_t* tile = P.tiles + (e * P.rts + rt) * P.kbs * lin_block_bytes(QB);
-    const float s = n < P.N ? __half2float(__ushort_as_half(P.scale[e * P.N + n])) : 0.0f;
-    const float bias = P.epi.bias && n < P.N ? lin_elem(P.epi.bias, e * P.N + n, P.epi.bias_bf16) : 0.0f;
-    for (int64_t m0 = a + 8 * blockIdx.y; m0 < b; m0 += 8 * gridDim.y) {
-        float acc[8] = {};
-        for (int64_t kb = 0; kb < P.kbs; ++kb) {
-            __syncthreads();
-            for (int i = r; i < 8 * kLinK; i += kLinRows) {
-                const int64_t m = m0 + i / kLinK, k = kb * kLinK + i % kLinK;
-                xs[i / kLinK][i % kLinK] = m < b && k < P.K ? bf16_bits_to_float(P.x[m * P.ldx + k]) : 0.0f;
+}
+
+// ------------------------------------------------------------- scheduling --
+
+// A unit of work: one tile of 128 weight rows by up to NT consecutive rows of X
+// of one expert.
+struct LinUnit {
+    int64_t e, m0, m1;           // expert, rows [m0, m1) of X
+    int32_t rt;                  // row tile
+    int32_t bad;                 // an offset out of order or range was met
+};
+
+// Unit `tt` of the token tiles (expert-major) found by one warp: every lane
+// scans its share of the experts' tile counts.  m0 = m1 past the last.
+__device__ __forceinline__ LinUnit lin_find(const LinParams& P, int64_t tt, int nt) {
+    LinUnit u{0, 0, 0, 0, 0};
+    if (!P.offsets) {
+        u.m0 = min(tt * nt, P.M);
+        u.m1 = min(u.m0 + nt, P.M);
+        return u;
+    }
+    const int lane = threadIdx.x & 31;
+    int64_t before = 0;                                    // tiles of the experts before this round's
+    for (int64_t e0 = 0; e0 < P.E; e0 += 32) {
+        const int64_t e = e0 + lane;
+        int64_t a = 0, b = 0;
+        bool ok = true;
+        if (e < P.E) {
+            const int32_t p = __ldg(P.offsets + e), q = __ldg(P.offsets + e + 1);
+            ok = p >= 0 && q >= p && q <= P.M;
+            a = ok ? p : 0;
+            b = ok ? q : 0;
+        }
+        if (!__all_sync(0xffffffffu, ok)) u.bad = 1;
+        const int64_t n = (b - a + nt - 1) / nt;
+        int64_t sum = n;                                   // inclusive prefix sum
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        const bool mine = tt >= before + sum - n && tt < before + sum;
+        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        if (who && u.m1 == 0) {
+            const int l = __ffs(who) - 1;
+            const int64_t m0 = a + (tt - before - (sum - n)) * nt;
+            u.e = e0 + l;
+            u.m0 = __shfl_sync(0xffffffffu, m0, l);
+            u.m1 = min(u.m0 + nt, __shfl_sync(0xffffffffu, b, l));
+            if (blockIdx.x != 0) return u;                 // block 0 reads on: every offset is checked
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return u;
+}
+
+// ----------------------------------------------------------------- kernel --
+//
+// One block per unit, or a cluster of `split` blocks that share its column
+// blocks.  The weight tile is the MMA's A operand, M = 128, and the tokens its B
+// operand, N = NT: a decode step pays for no padding of the tokens to 128 rows.
+// Warps:
+//   0       copies: a stage is two column blocks (128 of K): their codes by one
+//           bulk copy, the X tiles by TMA
+//   1       TMEM allocation, then the MMAs
+//   2 .. 9  codes -> bf16 integers in TMEM (A operand): group g takes column
+//           block g of each stage, thread r of a group's four warps weight row r;
+//           then the epilogue
+// Shared memory carries codes and X only, and a code costs about 1.6
+// instructions on the way (masks, shifts, one exact subtraction per pair); the
+// row scale waits until the epilogue.
+// With split > 1 the blocks put their sums into their own shared memory, and
+// after a cluster barrier each finishes its share of the elements, adding the
+// blocks' sums in rank order.
+constexpr int kLinThreads = 320;
+constexpr int kLinMaxStages = 8;
+
+template <int QB, int NT>
+struct LinShape {
+    static constexpr uint32_t x_block = NT * 128u;                       // one column block of X
+    static constexpr uint32_t c_block = lin_block_bytes(QB);
+    static constexpr uint32_t stage = 2 * (x_block + c_block);
+    static constexpr uint32_t acc_cols = NT <= 64 ? 64 : NT;
+    static constexpr uint32_t slots = (256 - acc_cols) / 64;             // stages of A in TMEM
+    static constexpr uint32_t bars = 8 * (2 * kLinMaxStages + 2 * 4 + 2) + 64;
+    static constexpr int smem(int stages) { return 1024 + stages * (int)stage + (int)bars; }
+};
+
+template <int QB, int NT>
+__global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_constant__ LinParams P) {
+    using S = LinShape<QB, NT>;
+    extern __shared__ unsigned char g_smem[];
+    __shared__ LinUnit s_unit;
+    const uint32_t base = (g_smem_u32(g_smem) + 1023u) & ~1023u;
+    const int D = P.stages;
+    const uint32_t bars = base + (uint32_t)D * S::stage;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (kLinMaxStages + s); };
+    auto wready = [&](int t) { return bars + 8u * (2 * kLinMaxStages + t); };
+    auto tfree = [&](int t) { return bars + 8u * (2 * kLinMaxStages + 4 + t); };
+    const uint32_t acc_full = bars + 8u * (2 * kLinMaxStages + 8);
+    const uint32_t tmem_slot = acc_full + 8u;
+    auto x_tile = [&](int s, int j) { return base + (uint32_t)s * S::stage + j * S::x_block; };
+    auto c_tile = [&](int s, int j) { return base + (uint32_t)s * S::stage + 2 * S::x_block + j * S::c_block; };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t rank = P.split > 1 ? (int32_t)(blockIdx.x % P.split) : 0;
+    const int64_t index = blockIdx.x / P.split;            // unit: token tile by row tile, row tiles fastest
+    if (warp == 2) {
+        LinUnit u = lin_find(P, index / P.rts, NT);
+        u.rt = (int32_t)(index % P.rts);
+        if (lane == 0) {
+            s_unit = u;
+            if (u.bad && P.status) atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x8u);
+        }
+    } else if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(tmem_slot) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (threadIdx.x == 0) {
+        for (int s = 0; s < D; ++s) {
+            g_bar_init(full(s), 1);
+            g_bar_init(empty(s), 1);
+        }
+        for (int t = 0; t < (int)S::slots; ++t) {
+            g_bar_init(wready(t), 8);
+            g_bar_init(tfree(t), 1);
+        }
+        g_bar_init(acc_full, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.tmap_x)) : "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
+    const LinUnit u = s_unit;
+    const int mv = (int)(u.m1 - u.m0);                     // rows of X in the unit
+    // this block's column blocks, two a stage
+    const int kb0 = (int)((int64_t)P.kbs * rank / P.split), kb1 = (int)((int64_t)P.kbs * (rank + 1) / P.split);
+    const int stages = mv > 0 ? (kb1 - kb0 + 1) / 2 : 0;
+    bool ok = true;
+    if (warp == 0) {
+        const uint8_t* codes = P.tiles + ((u.e * P.rts + u.rt) * P.kbs + kb0) * (int64_t)S::c_block;
+        int s = 0;
+        uint32_t ph = 0u;
+        int issued = 0;
+        for (; issued < stages; ++issued) {
+            if (issued >= D && !g_wait_warp(empty(s), ph ^ 1u)) {
+                ok = false;
+                break;
             }
-            __syncthreads();
-            const uint4* src = reinterpret_cast<const uint4*>(tile + kb * lin_block_bytes(QB)) + r;
-            uint32_t w[16], o[32];
-#pragma unroll
-            for (int c = 0; c < (QB == 6 ? 3 : 4); ++c) {
-                const uint4 u = src[c * kLinRows];
-                w[4 * c] = u.x; w[4 * c + 1] = u.y; w[4 * c + 2] = u.z; w[4 * c + 3] = u.w;
+            if (lane == 0) {
+                const int kb = kb0 + 2 * issued, n = min(2, kb1 - kb);
+                g_arrive_tx(full(s), (uint32_t)n * (S::x_block + S::c_block));
+                lin_bulk_load(c_tile(s, 0), codes, (uint32_t)n * S::c_block, full(s));
+                codes += n * S::c_block;
+                for (int j = 0; j < n; ++j)
+                    g_tma_load_2d(x_tile(s, j), &P.tmap_x, (kb + j) * kLinK, (int)u.m0, full(s));
             }
-            if constexpr (QB == 6) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t t[8];
-                    lin_codes6(w[3 * g], w[3 * g + 1], w[3 * g + 2], t);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) o[8 * g + j] = t[j];
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) lin_codes8(w[j], o[2 * j], o[2 * j + 1]);
-            }
-#pragma unroll
-            for (int i = 0; i < kLinK; ++i) {
-                const float q = (i & 1) ? __uint_as_float(o[i >> 1] & 0xFFFF0000u) : __uint_as_float(o[i >> 1] << 16);
-#pragma unroll
-                for (int t = 0; t < 8; ++t) acc[t] += xs[t][i] * q;
+            if (++s == D) {
+                s = 0;
+                ph ^= 1u;
             }
         }
-        if (n < P.N)
-            for (int t = 0; t < 8; ++t)
-                if (m0 + t < b) lin_finish(P.epi, acc[t], s, bias, m0 + t, n);
+        // no copy may still be landing when the block reuses or leaves its memory
+        for (int q = max(0, issued - D); q < issued; ++q)
+            if (!g_wait_warp(full(q % D), (uint32_t)((q / D) & 1))) ok = false;
+    } else if (warp == 1) {
+        int s = 0, t = 0;
+        uint32_t ph = 0u, tph = 0u;
+        for (int i = 0; i < stages; ++i) {
+            if (!g_wait_warp(full(s), ph) || !g_wait_warp(wready(t), tph)) {
+                ok = false;
+                break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const int n = min(2, kb1 - kb0 - 2 * i);
+            for (int j = 0; j < n; ++j)
+                g_mma_stage_ts(tmem, tmem + S::acc_cols + 64u * t + 32u * j, x_tile(s, j), P.idesc, i | j ? 1u : 0u);
+            g_commit(empty(s));
+            g_commit(tfree(t));
+            if (++s == D) {
+                s = 0;
+                ph ^= 1u;
+            }
+            if (++t == (int)S::slots) {
+                t = 0;
+                tph ^= 1u;
+            }
+        }
+        g_commit(acc_full);                                // every MMA issued is done
+        if (!g_wait_warp(acc_full, 0u)) ok = false;
+    } else {
+        const int grp = (warp - 2) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        int s = 0, t = 0;
+        uint32_t ph = 0u, tph = 0u;
+        for (int i = 0; i < stages; ++i) {
+            if (!g_wait_warp(full(s), ph) || (i >= (int)S::slots && !g_wait_warp(tfree(t), tph ^ 1u))) {
+                ok = false;
+                break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (kb0 + 2 * i + grp < kb1) {
+                lin_codes_to_tmem<QB>(c_tile(s, grp) + 16u * r, tmem + lanes + S::acc_cols + 64u * t + 32u * grp);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) g_arrive(wready(t));
+            if (++s == D) {
+                s = 0;
+                ph ^= 1u;
+            }
+            if (++t == (int)S::slots) {
+                t = 0;
+                tph ^= 1u;
+            }
+        }
+        if (!g_wait_warp(acc_full, 0u)) ok = false;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (stages > 0) {
+            const int64_t n = (int64_t)u.rt * kLinRows + r;
+            const bool in = n < P.N;
+            float sc = 0.0f, bi = 0.0f;
+            if (P.split == 1 && in) {
+                sc = __half2float(__ushort_as_half(P.scale[u.e * P.N + n]));
+                if (P.epi.bias) bi = lin_elem(P.epi.bias, u.e * P.N + n, P.epi.bias_bf16);
+            }
+            for (int c0 = 8 * grp; c0 < mv; c0 += 16) {    // the groups take turns of 8 tokens
+                float v[8];
+                lin_tmem_ld8(tmem + lanes + (uint32_t)c0, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (c0 + i >= mv) break;
+                    if (P.split > 1)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + 4u * (uint32_t)((c0 + i) * kLinRows + r)),
+                                     "f"(v[i])
+                                     : "memory");
+                    else if (in)
+                        lin_finish(P.epi, v[i], sc, bi, u.m0 + c0 + i, n);
+                }
+            }
+        }
+    }
+    if (!ok && lane == 0 && P.status) atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x4u);
+    __syncwarp();
+    if (P.split > 1 && mv > 0) {                           // the same in every block of the cluster
+        lin_cluster_sync();
+        for (int i = rank * kLinThreads + (int)threadIdx.x; i < mv * kLinRows; i += P.split * kLinThreads) {
+            const int64_t n = (int64_t)u.rt * kLinRows + i % kLinRows;
+            if (n >= P.N) continue;
+            float v = 0.0f;
+            for (int q = 0; q < P.split; ++q) v += lin_ld_peer(base + 4u * (uint32_t)i, (uint32_t)q);
+            const float sc = __half2float(__ushort_as_half(P.scale[u.e * P.N + n]));
+            const float bi = P.epi.bias ? lin_elem(P.epi.bias, u.e * P.N + n, P.epi.bias_bf16) : 0.0f;
+            lin_finish(P.epi, v, sc, bi, u.m0 + i / kLinRows, n);
+        }
+        lin_cluster_sync();                                // its memory is read until here
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (warp == 1) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem) : "memory");
+    }
+}
+
+// K = 0: the sums are 0, the epilogue is all there is.  One block per row of Y.
+__global__ void __launch_bounds__(256) linear_empty_kernel(const __grid_constant__ LinParams P) {
+    for (int64_t m = blockIdx.x; m < P.M; m += gridDim.x) {
+        int64_t e = 0;
+        if (P.offsets) {                                   // the expert of the row: the last that begins at or before it
+            int64_t lo = 0, hi = P.E;
+            while (hi - lo > 1) {
+                const int64_t mid = (lo + hi) >> 1;
+                if (P.offsets[mid] <= m) lo = mid;
+                else hi = mid;
+            }
+            e = lo;
+            if (m < P.offsets[e] || m >= P.offsets[e + 1]) continue;
+        }
+        for (int64_t n = threadIdx.x; n < P.N; n += blockDim.x)
+            lin_finish(P.epi, 0.0f, 0.0f, P.epi.bias ? lin_elem(P.epi.bias, e * P.N + n, P.epi.bias_bf16) : 0.0f, m, n);
     }
 }
 
