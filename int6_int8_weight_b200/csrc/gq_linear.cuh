@@ -71,34 +71,43 @@ __global__ void __launch_bounds__(kLinRows) tile_weight_kernel(const uint8_t* __
 
 // ----------------------------------------------------------------- codes --
 
-__device__ __forceinline__ uint32_t lin_sub2(uint32_t a, uint32_t b) {
+// a * b + c on bf16 pairs (one instruction; the pair subtraction is several).
+__device__ __forceinline__ uint32_t lin_fma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+// (a & b) | c in one instruction: written out, because with two constants the
+// compiler takes a masking and an or-ing one.
+__device__ __forceinline__ uint32_t lin_and_or(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
 
 // The 8 pairs of codes of one int6 group (three words) as bf16x2 integers.  A
 // 6-bit field u in a half's low bits under 0x4300 is the bf16 number 128 + u; less
 // 160 it is q, exactly.
-__device__ __forceinline__ void lin_codes6(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t (&o)[8]) {
-    constexpr uint32_t m = 0x003F003Fu, h = 0x43004300u, s = 0x43204320u;
-    o[0] = lin_sub2((w0 & m) | h, s);
-    o[1] = lin_sub2((w1 & m) | h, s);
-    o[2] = lin_sub2((w2 & m) | h, s);
-    o[3] = lin_sub2((w0 >> 6 & m) | h, s);
-    o[4] = lin_sub2((w1 >> 6 & m) | h, s);
-    o[5] = lin_sub2((w2 >> 6 & m) | h, s);
-    o[6] = lin_sub2((w0 >> 12 & 0x000F000Fu) | ((w2 >> 8 & 0x00300030u) | h), s);
-    o[7] = lin_sub2((w1 >> 12 & 0x000F000Fu) | ((w2 >> 10 & 0x00300030u) | h), s);
+__device__ __forceinline__ void lin_codes6(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t* o) {
+    constexpr uint32_t m = 0x003F003Fu, h = 0x43004300u, one = 0x3F803F80u, s = 0xC320C320u;
+    o[0] = lin_fma2(lin_and_or(w0, m, h), one, s);
+    o[1] = lin_fma2(lin_and_or(w1, m, h), one, s);
+    o[2] = lin_fma2(lin_and_or(w2, m, h), one, s);
+    o[3] = lin_fma2(lin_and_or(w0 >> 6, m, h), one, s);
+    o[4] = lin_fma2(lin_and_or(w1 >> 6, m, h), one, s);
+    o[5] = lin_fma2(lin_and_or(w2 >> 6, m, h), one, s);
+    o[6] = lin_fma2(lin_and_or(w0 >> 12, 0x000F000Fu, lin_and_or(w2 >> 8, 0x00300030u, h)), one, s);
+    o[7] = lin_fma2(lin_and_or(w1 >> 12, 0x000F000Fu, lin_and_or(w2 >> 10, 0x00300030u, h)), one, s);
 }
 
 // The two pairs of an int8 word: the low seven bits give 128 + low, the sign bit
 // under 0x4300 is 128 or 256, and their difference is q, exactly.
 __device__ __forceinline__ void lin_codes8(uint32_t w, uint32_t& a, uint32_t& b) {
-    constexpr uint32_t m = 0x007F007Fu, t = 0x00800080u, h = 0x43004300u;
+    constexpr uint32_t m = 0x007F007Fu, t = 0x00800080u, h = 0x43004300u, minus = 0xBF80BF80u;
     const uint32_t v = w >> 8;
-    a = lin_sub2((w & m) | h, (w & t) | h);
-    b = lin_sub2((v & m) | h, (v & t) | h);
+    a = lin_fma2(lin_and_or(w, t, h), minus, lin_and_or(w, m, h));
+    b = lin_fma2(lin_and_or(v, t, h), minus, lin_and_or(v, m, h));
 }
 
 // -------------------------------------------------------------- epilogue --
@@ -189,31 +198,32 @@ __device__ __forceinline__ void lin_cluster_sync() {
 // thread's lane: column j holds k = 2j and 2j + 1 as bf16.
 template <int QB>
 __device__ __forceinline__ void lin_codes_to_tmem(uint32_t src, uint32_t taddr) {
-    constexpr int kChunks = QB == 6 ? 3 : 4;
-    uint32_t w[4 * kChunks];
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c)
+    auto chunk = [&](int c, uint32_t* w) {
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                      : "r"(src + 16u * kLinRows * c)
                      : "memory");
+    };
+    uint32_t w[16], o[16];
+    chunk(0, w);
+    chunk(1, w + 4);
+    if constexpr (QB == 6) {
+        chunk(2, w + 8);
+        lin_codes6(w[0], w[1], w[2], o);
+        lin_codes6(w[3], w[4], w[5], o + 8);
+        g_tmem_st16(taddr, o);
+        lin_codes6(w[6], w[7], w[8], o);
+        lin_codes6(w[9], w[10], w[11], o + 8);
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t o[16];
-        if constexpr (QB == 6) {
+        for (int j = 0; j < 8; ++j) lin_codes8(w[j], o[2 * j], o[2 * j + 1]);
+        chunk(2, w);
+        chunk(3, w + 4);
+        g_tmem_st16(taddr, o);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t t[8];
-                lin_codes6(w[6 * h + 3 * g], w[6 * h + 3 * g + 1], w[6 * h + 3 * g + 2], t);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[8 * g + j] = t[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) lin_codes8(w[8 * h + j], o[2 * j], o[2 * j + 1]);
-        }
-        g_tmem_st16(taddr + 16u * h, o);
+        for (int j = 0; j < 8; ++j) lin_codes8(w[j], o[2 * j], o[2 * j + 1]);
     }
+    g_tmem_st16(taddr + 16u, o);
 }
 
 // ------------------------------------------------------------- scheduling --
@@ -279,16 +289,17 @@ __device__ __forceinline__ LinUnit lin_find(const LinParams& P, int64_t tt, int 
 //   0       copies: a stage is two column blocks (128 of K): their codes by one
 //           bulk copy, the X tiles by TMA
 //   1       TMEM allocation, then the MMAs
-//   2 .. 9  codes -> bf16 integers in TMEM (A operand): group g takes column
-//           block g of each stage, thread r of a group's four warps weight row r;
-//           then the epilogue
+//   2 .. 17 codes -> bf16 integers in TMEM (A operand): four groups of four
+//           warps, group g takes column block g % 2 of every other stage, thread
+//           r of a group weight row r; then the epilogue
 // Shared memory carries codes and X only, and a code costs about 1.6
 // instructions on the way (masks, shifts, one exact subtraction per pair); the
 // row scale waits until the epilogue.
 // With split > 1 the blocks put their sums into their own shared memory, and
 // after a cluster barrier each finishes its share of the elements, adding the
 // blocks' sums in rank order.
-constexpr int kLinThreads = 320;
+constexpr int kLinGroups = 4;
+constexpr int kLinThreads = 64 + 128 * kLinGroups;
 constexpr int kLinMaxStages = 8;
 
 template <int QB, int NT>
@@ -355,6 +366,13 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     // this block's column blocks, two a stage
     const int kb0 = (int)((int64_t)P.kbs * rank / P.split), kb1 = (int)((int64_t)P.kbs * (rank + 1) / P.split);
     const int stages = mv > 0 ? (kb1 - kb0 + 1) / 2 : 0;
+    // the weight row that this thread's elements of Y belong to, in either form of the epilogue
+    const int64_t n = (int64_t)u.rt * kLinRows + (P.split > 1 ? threadIdx.x & 127 : 32 * (warp & 3) + lane);
+    float sc = 0.0f, bi = 0.0f;
+    if (mv > 0 && n < P.N) {
+        sc = __half2float(__ushort_as_half(P.scale[u.e * P.N + n]));
+        if (P.epi.bias) bi = lin_elem(P.epi.bias, u.e * P.N + n, P.epi.bias_bf16);
+    }
     bool ok = true;
     if (warp == 0) {
         const uint8_t* codes = P.tiles + ((u.e * P.rts + u.rt) * P.kbs + kb0) * (int64_t)S::c_block;
@@ -410,41 +428,36 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     } else {
         const int grp = (warp - 2) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        int s = 0, t = 0;
+        constexpr int kStep = kLinGroups / 2;              // stages from one of a group's to its next
+        int s = grp >> 1, t = grp >> 1;
         uint32_t ph = 0u, tph = 0u;
-        for (int i = 0; i < stages; ++i) {
+        for (int i = grp >> 1; i < stages; i += kStep) {
             if (!g_wait_warp(full(s), ph) || (i >= (int)S::slots && !g_wait_warp(tfree(t), tph ^ 1u))) {
                 ok = false;
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            if (kb0 + 2 * i + grp < kb1) {
-                lin_codes_to_tmem<QB>(c_tile(s, grp) + 16u * r, tmem + lanes + S::acc_cols + 64u * t + 32u * grp);
+            if (kb0 + 2 * i + (grp & 1) < kb1) {
+                lin_codes_to_tmem<QB>(c_tile(s, grp & 1) + 16u * r,
+                                      tmem + lanes + S::acc_cols + 64u * t + 32u * (grp & 1));
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0) g_arrive(wready(t));
-            if (++s == D) {
-                s = 0;
+            if ((s += kStep) >= D) {
+                s -= D;
                 ph ^= 1u;
             }
-            if (++t == (int)S::slots) {
-                t = 0;
+            if ((t += kStep) >= (int)S::slots) {
+                t -= (int)S::slots;
                 tph ^= 1u;
             }
         }
         if (!g_wait_warp(acc_full, 0u)) ok = false;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if (stages > 0) {
-            const int64_t n = (int64_t)u.rt * kLinRows + r;
-            const bool in = n < P.N;
-            float sc = 0.0f, bi = 0.0f;
-            if (P.split == 1 && in) {
-                sc = __half2float(__ushort_as_half(P.scale[u.e * P.N + n]));
-                if (P.epi.bias) bi = lin_elem(P.epi.bias, u.e * P.N + n, P.epi.bias_bf16);
-            }
-            for (int c0 = 8 * grp; c0 < mv; c0 += 16) {    // the groups take turns of 8 tokens
+            for (int c0 = 8 * grp; c0 < mv; c0 += 8 * kLinGroups) {   // the groups take turns of 8 tokens
                 float v[8];
                 lin_tmem_ld8(tmem + lanes + (uint32_t)c0, v);
 #pragma unroll
@@ -454,7 +467,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
                         asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + 4u * (uint32_t)((c0 + i) * kLinRows + r)),
                                      "f"(v[i])
                                      : "memory");
-                    else if (in)
+                    else if (n < P.N)
                         lin_finish(P.epi, v[i], sc, bi, u.m0 + c0 + i, n);
                 }
             }
@@ -464,15 +477,16 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     __syncwarp();
     if (P.split > 1 && mv > 0) {                           // the same in every block of the cluster
         lin_cluster_sync();
-        for (int i = rank * kLinThreads + (int)threadIdx.x; i < mv * kLinRows; i += P.split * kLinThreads) {
-            const int64_t n = (int64_t)u.rt * kLinRows + i % kLinRows;
-            if (n >= P.N) continue;
-            float v = 0.0f;
-            for (int q = 0; q < P.split; ++q) v += lin_ld_peer(base + 4u * (uint32_t)i, (uint32_t)q);
-            const float sc = __half2float(__ushort_as_half(P.scale[u.e * P.N + n]));
-            const float bi = P.epi.bias ? lin_elem(P.epi.bias, u.e * P.N + n, P.epi.bias_bf16) : 0.0f;
-            lin_finish(P.epi, v, sc, bi, u.m0 + i / kLinRows, n);
-        }
+        // rows of Y by 128 threads each over the cluster; a thread keeps its column
+        constexpr int kLines = kLinThreads / kLinRows;
+        const int line = (int)threadIdx.x / kLinRows;
+        if (line < kLines && n < P.N)
+            for (int c = rank * kLines + line; c < mv; c += P.split * kLines) {
+                const uint32_t at = base + 4u * (uint32_t)(c * kLinRows + ((int)threadIdx.x & 127));
+                float v = 0.0f;
+                for (int q = 0; q < P.split; ++q) v += lin_ld_peer(at, (uint32_t)q);
+                lin_finish(P.epi, v, sc, bi, u.m0 + c, n);
+            }
         lin_cluster_sync();                                // its memory is read until here
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
