@@ -37,10 +37,12 @@ gq_status launch(LinParams& P, const void* d_x, int64_t K, int64_t ldx, cudaStre
     // token tiles: exact for one weight; for experts the most that any offsets can give
     const int64_t tts = P.offsets ? P.M / NT + std::min<int64_t>(P.E, P.M) : (P.M + NT - 1) / NT;
     const int64_t units = tts * P.rts;
-    int split = 1;
-    while (split < 8 && units * split * 2 <= 2 * (int64_t)sm_count() && P.kbs >= 4 * split) split *= 2;
-    if (units * split > INT32_MAX) return GQ_ERR_UNSUPPORTED;
-    P.split = split;
+    if (units > INT32_MAX) return GQ_ERR_UNSUPPORTED;
+    int ls = 0;
+    while (ls < 3 && (units << (ls + 1)) <= 2 * (int64_t)sm_count() && P.kbs >= 4 << ls) ++ls;
+    if (units << ls > INT32_MAX) return GQ_ERR_UNSUPPORTED;
+    P.log_split = ls;
+    const int split = 1 << ls;
     // two blocks to an SM
     P.stages = std::min<int>(kLinMaxStages, (kLinSmem - S::smem(0)) / (int)S::stage);
     const int smem = std::max(S::smem(P.stages), split > 1 ? S::smem(0) + NT * kLinRows * 4 : 0);

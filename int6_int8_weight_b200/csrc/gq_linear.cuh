@@ -154,7 +154,7 @@ struct LinParams {
     int32_t* status;
     int64_t M, N, E;
     int32_t kbs, rts;            // column blocks, row tiles of a weight
-    int32_t split;               // blocks (a cluster) that share a tile's column blocks
+    int32_t log_split;           // 2^this blocks (a cluster) share a tile's column blocks
     int32_t stages;              // ring depth
     uint32_t idesc;
     LinEpi epi;
@@ -231,58 +231,60 @@ __device__ __forceinline__ void lin_codes_to_tmem(uint32_t src, uint32_t taddr) 
 // A unit of work: one tile of 128 weight rows by up to NT consecutive rows of X
 // of one expert.
 struct LinUnit {
-    int64_t e, m0, m1;           // expert, rows [m0, m1) of X
+    int32_t e, m0, m1;           // expert, rows [m0, m1) of X
     int32_t rt;                  // row tile
     int32_t bad;                 // an offset out of order or range was met
 };
 
 // Unit `tt` of the token tiles (expert-major) found by one warp: every lane
 // scans its share of the experts' tile counts.  m0 = m1 past the last.
-__device__ __forceinline__ LinUnit lin_find(const LinParams& P, int64_t tt, int nt) {
+template <int NT>
+__device__ __forceinline__ LinUnit lin_find(const LinParams& P, int tt) {
     LinUnit u{0, 0, 0, 0, 0};
+    const int M = (int)P.M;
     if (!P.offsets) {
-        u.m0 = min(tt * nt, P.M);
-        u.m1 = min(u.m0 + nt, P.M);
+        u.m0 = tt * NT;
+        u.m1 = min(M - u.m0, NT) + u.m0;
         return u;
     }
     const int lane = threadIdx.x & 31;
-    int64_t before = 0;                                    // tiles of the experts before this round's
-    for (int64_t e0 = 0; e0 < P.E; e0 += 32) {
-        const int64_t e = e0 + lane;
-        int64_t a = 0, b = 0;
+    int before = 0;                                        // tiles of the experts before this round's
+    for (int e0 = 0; e0 < (int)P.E; e0 += 32) {
+        const int e = e0 + lane;
+        int a = 0, b = 0;
         bool ok = true;
-        if (e < P.E) {
-            const int32_t p = __ldg(P.offsets + e), q = __ldg(P.offsets + e + 1);
-            ok = p >= 0 && q >= p && q <= P.M;
+        if (e < (int)P.E) {
+            const int p = __ldg(P.offsets + e), q = __ldg(P.offsets + e + 1);
+            ok = p >= 0 && q >= p && q <= M;
             a = ok ? p : 0;
             b = ok ? q : 0;
         }
         if (!__all_sync(0xffffffffu, ok)) u.bad = 1;
-        const int64_t n = (b - a + nt - 1) / nt;
-        int64_t sum = n;                                   // inclusive prefix sum
+        const int n = (int)(((unsigned)(b - a) + NT - 1u) / NT);
+        // inclusive prefix sum, held at 2^30 (only offsets that are out of order could carry it past the rows' number)
+        int sum = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += o;
+            const int o = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum = (int)min((unsigned)sum + (unsigned)o, 1u << 30);
         }
-        const bool mine = tt >= before + sum - n && tt < before + sum;
-        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        const int at = (int)min((unsigned)before + (unsigned)sum, 1u << 30);   // tiles up to and with this expert's
+        const uint32_t who = __ballot_sync(0xffffffffu, n > 0 && tt < at && tt >= at - n);
         if (who && u.m1 == 0) {
             const int l = __ffs(who) - 1;
-            const int64_t m0 = a + (tt - before - (sum - n)) * nt;
             u.e = e0 + l;
-            u.m0 = __shfl_sync(0xffffffffu, m0, l);
-            u.m1 = min(u.m0 + nt, __shfl_sync(0xffffffffu, b, l));
+            u.m0 = __shfl_sync(0xffffffffu, a + (tt - (at - n)) * NT, l);
+            u.m1 = min(__shfl_sync(0xffffffffu, b, l) - u.m0, NT) + u.m0;
             if (blockIdx.x != 0) return u;                 // block 0 reads on: every offset is checked
         }
-        before += __shfl_sync(0xffffffffu, sum, 31);
+        before = __shfl_sync(0xffffffffu, at, 31);
     }
     return u;
 }
 
 // ----------------------------------------------------------------- kernel --
 //
-// One block per unit, or a cluster of `split` blocks that share its column
+// One block per unit, or a cluster of 2^log_split blocks that share its column
 // blocks.  The weight tile is the MMA's A operand, M = 128, and the tokens its B
 // operand, N = NT: a decode step pays for no padding of the tokens to 128 rows.
 // Warps:
@@ -295,7 +297,7 @@ __device__ __forceinline__ LinUnit lin_find(const LinParams& P, int64_t tt, int 
 // Shared memory carries codes and X only, and a code costs about 1.6
 // instructions on the way (masks, shifts, one exact subtraction per pair); the
 // row scale waits until the epilogue.
-// With split > 1 the blocks put their sums into their own shared memory, and
+// With a split the blocks put their sums into their own shared memory, and
 // after a cluster barrier each finishes its share of the elements, adding the
 // blocks' sums in rank order.
 constexpr int kLinGroups = 4;
@@ -331,11 +333,13 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     auto c_tile = [&](int s, int j) { return base + (uint32_t)s * S::stage + 2 * S::x_block + j * S::c_block; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t rank = P.split > 1 ? (int32_t)(blockIdx.x % P.split) : 0;
-    const int64_t index = blockIdx.x / P.split;            // unit: token tile by row tile, row tiles fastest
+    // the split is a power of two; 32-bit arithmetic throughout (a 64-bit division costs more than a block of codes)
+    const uint32_t split = 1u << P.log_split, rank = blockIdx.x & (split - 1u);
+    const uint32_t index = blockIdx.x >> P.log_split;      // unit: token tile by row tile, row tiles fastest
     if (warp == 2) {
-        LinUnit u = lin_find(P, index / P.rts, NT);
-        u.rt = (int32_t)(index % P.rts);
+        const uint32_t tt = index / (uint32_t)P.rts;
+        LinUnit u = lin_find<NT>(P, (int)tt);
+        u.rt = (int32_t)(index - tt * (uint32_t)P.rts);
         if (lane == 0) {
             s_unit = u;
             if (u.bad && P.status) atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x8u);
@@ -362,20 +366,20 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
     const LinUnit u = s_unit;
-    const int mv = (int)(u.m1 - u.m0);                     // rows of X in the unit
+    const int mv = u.m1 - u.m0;                            // rows of X in the unit
     // this block's column blocks, two a stage
-    const int kb0 = (int)((int64_t)P.kbs * rank / P.split), kb1 = (int)((int64_t)P.kbs * (rank + 1) / P.split);
+    const int kb0 = (int)((uint32_t)P.kbs * rank >> P.log_split), kb1 = (int)((uint32_t)P.kbs * (rank + 1) >> P.log_split);
     const int stages = mv > 0 ? (kb1 - kb0 + 1) / 2 : 0;
     // the weight row that this thread's elements of Y belong to, in either form of the epilogue
-    const int64_t n = (int64_t)u.rt * kLinRows + (P.split > 1 ? threadIdx.x & 127 : 32 * (warp & 3) + lane);
+    const int64_t n = (int64_t)u.rt * kLinRows + (split > 1 ? threadIdx.x & 127 : 32 * (warp & 3) + lane);
     float sc = 0.0f, bi = 0.0f;
     if (mv > 0 && n < P.N) {
-        sc = __half2float(__ushort_as_half(P.scale[u.e * P.N + n]));
-        if (P.epi.bias) bi = lin_elem(P.epi.bias, u.e * P.N + n, P.epi.bias_bf16);
+        sc = __half2float(__ushort_as_half(P.scale[(int64_t)u.e * P.N + n]));
+        if (P.epi.bias) bi = lin_elem(P.epi.bias, (int64_t)u.e * P.N + n, P.epi.bias_bf16);
     }
     bool ok = true;
     if (warp == 0) {
-        const uint8_t* codes = P.tiles + ((u.e * P.rts + u.rt) * P.kbs + kb0) * (int64_t)S::c_block;
+        const uint8_t* codes = P.tiles + (((int64_t)u.e * P.rts + u.rt) * P.kbs + kb0) * (int64_t)S::c_block;
         int s = 0;
         uint32_t ph = 0u;
         int issued = 0;
@@ -463,29 +467,29 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if (c0 + i >= mv) break;
-                    if (P.split > 1)
+                    if (split > 1)
                         asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + 4u * (uint32_t)((c0 + i) * kLinRows + r)),
                                      "f"(v[i])
                                      : "memory");
                     else if (n < P.N)
-                        lin_finish(P.epi, v[i], sc, bi, u.m0 + c0 + i, n);
+                        lin_finish(P.epi, v[i], sc, bi, (int64_t)u.m0 + c0 + i, n);
                 }
             }
         }
     }
     if (!ok && lane == 0 && P.status) atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x4u);
     __syncwarp();
-    if (P.split > 1 && mv > 0) {                           // the same in every block of the cluster
+    if (split > 1 && mv > 0) {                           // the same in every block of the cluster
         lin_cluster_sync();
         // rows of Y by 128 threads each over the cluster; a thread keeps its column
         constexpr int kLines = kLinThreads / kLinRows;
         const int line = (int)threadIdx.x / kLinRows;
         if (line < kLines && n < P.N)
-            for (int c = rank * kLines + line; c < mv; c += P.split * kLines) {
+            for (int c = (int)rank * kLines + line; c < mv; c += (int)split * kLines) {
                 const uint32_t at = base + 4u * (uint32_t)(c * kLinRows + ((int)threadIdx.x & 127));
                 float v = 0.0f;
-                for (int q = 0; q < P.split; ++q) v += lin_ld_peer(at, (uint32_t)q);
-                lin_finish(P.epi, v, sc, bi, u.m0 + c, n);
+                for (int q = 0; q < (int)split; ++q) v += lin_ld_peer(at, (uint32_t)q);
+                lin_finish(P.epi, v, sc, bi, (int64_t)u.m0 + c, n);
             }
         lin_cluster_sync();                                // its memory is read until here
     }
