@@ -45,6 +45,7 @@ gq_status launch(LinParams& P, const void* d_x, int64_t K, int64_t ldx, cudaStre
     const int split = 1 << ls;
     // two blocks to an SM
     P.stages = std::min<int>(kLinMaxStages, (kLinSmem - S::smem(0)) / (int)S::stage);
+    if (P.stages < (int)S::slots) return GQ_ERR_UNSUPPORTED;   // never: the conversion's waits need it
     const int smem = std::max(S::smem(P.stages), split > 1 ? S::smem(0) + NT * kLinRows * 4 : 0);
     int dev = 0;
     if (cuda_status(cudaGetDevice(&dev)) != GQ_OK) return GQ_ERR_CUDA;

@@ -433,10 +433,14 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
         const int grp = (warp - 2) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         constexpr int kStep = kLinGroups / 2;              // stages from one of a group's to its next
+        static_assert(kStep <= (int)S::slots, "the parity tests below");
         int s = grp >> 1, t = grp >> 1;
         uint32_t ph = 0u, tph = 0u;
         for (int i = grp >> 1; i < stages; i += kStep) {
-            if (!g_wait_warp(full(s), ph) || (i >= (int)S::slots && !g_wait_warp(tfree(t), tph ^ 1u))) {
+            // The slot first: once stage i - slots is done, stage i - stages (no later, the ring being at least as deep)
+            // has landed, so a parity test of full(s) cannot take an older phase for this one; nor can one of
+            // tfree(t), since the group's last stage was at most `slots` before.
+            if ((i >= (int)S::slots && !g_wait_warp(tfree(t), tph ^ 1u)) || !g_wait_warp(full(s), ph)) {
                 ok = false;
                 break;
             }
