@@ -554,7 +554,7 @@ GQ_API gq_status gq_gemm_grouped(const void* d_x, int64_t M, int64_t K, int64_t 
  * A non-finite gradient reaches p, m and v as the formulas say (32-bit); in an
  * 8-bit block whose m' or v' has a NaN or an infinity the new codes and
  * scales of that block are unspecified.
- * Asynchronous on `stream`; one launch per 200 tensors.
+ * Asynchronous on `stream`; one launch per 200 tensors of a state size.
  * Source: AdamW with decoupled weight decay (PR #69, PR #1414).
  */
 typedef struct gq_adamw_tensor {

@@ -62,39 +62,43 @@ extern "C" gq_status gq_adamw_step(const gq_adamw_tensor* t, int n, const gq_ada
     P.d_step = h->d_step;
     P.d_lr = h->d_lr;
     P.d_grad_scale = h->d_grad_scale;
-    for (int base = 0; base < n; base += kAdamDesc) {
-        const int nd = std::min(kAdamDesc, n - base);
-        int64_t items = 0;
-        P.ndesc = 0;
-        for (int i = 0; i < nd; ++i) {
-            const gq_adamw_tensor& T = t[base + i];
-            if (T.numel == 0) continue;
-            AdamDesc& D = P.d[P.ndesc];
-            D.p = T.p;
-            D.g = T.g;
-            D.m = T.m;
-            D.v = T.v;
-            D.ms = T.m_scale;
-            D.vs = T.v_scale;
-            D.copy = T.p_copy;
-            D.numel = T.numel;
-            D.wd = T.weight_decay;
-            D.decay = (float)(1.0 - h->lr * T.weight_decay);
-            D.key = (uint32_t)h->seed + (uint32_t)(base + i) * kAdamTensorMul;
-            const size_t sa = T.state_bits == 8 ? 8 : 16;
-            const bool vec = aligned(T.p, 16) && aligned(T.g, 16) && aligned(T.m, sa) && aligned(T.v, sa) &&
-                             (!T.p_copy || aligned(T.p_copy, 16));
-            D.flags = (T.p_dtype == GQ_BF16 ? kAdamPBf16 : 0) | (T.g_dtype == GQ_BF16 ? kAdamGBf16 : 0) |
-                      (T.state_bits == 8 ? kAdamState8 : 0) | (vec ? kAdamVec : 0);
-            D.pad = 0;
-            P.start[P.ndesc++] = items;
-            items += (T.numel + kAdamItem - 1) / kAdamItem;
+    // the tensors with 8-bit states and those with 32-bit ones, up to kAdamDesc a launch
+    for (const bool s8 : {false, true}) {
+        int i = 0;
+        while (i < n) {
+            int64_t items = 0;
+            P.ndesc = 0;
+            for (; i < n && P.ndesc < kAdamDesc; ++i) {
+                const gq_adamw_tensor& T = t[i];
+                if (T.numel == 0 || (T.state_bits == 8) != s8) continue;
+                AdamDesc& D = P.d[P.ndesc];
+                D.p = T.p;
+                D.g = T.g;
+                D.m = T.m;
+                D.v = T.v;
+                D.ms = T.m_scale;
+                D.vs = T.v_scale;
+                D.copy = T.p_copy;
+                D.numel = T.numel;
+                D.wd = T.weight_decay;
+                D.decay = (float)(1.0 - h->lr * T.weight_decay);
+                D.key = (uint32_t)h->seed + (uint32_t)i * kAdamTensorMul;
+                const size_t sa = s8 ? 8 : 16;
+                const bool vec = aligned(T.p, 16) && aligned(T.g, 16) && aligned(T.m, sa) && aligned(T.v, sa) &&
+                                 (!T.p_copy || aligned(T.p_copy, 16));
+                D.flags = (T.p_dtype == GQ_BF16 ? kAdamPBf16 : 0) | (T.g_dtype == GQ_BF16 ? kAdamGBf16 : 0) |
+                          (vec ? kAdamVec : 0);
+                D.pad = 0;
+                P.start[P.ndesc++] = items;
+                items += (T.numel + kAdamItem - 1) / kAdamItem;
+            }
+            P.start[P.ndesc] = items;
+            if (items == 0) continue;
+            const unsigned blocks = (unsigned)std::min<int64_t>(items, (int64_t)sm_count() * 32);
+            if (s8) adamw_kernel<true><<<blocks, kAdamThreads, 0, stream>>>(P);
+            else adamw_kernel<false><<<blocks, kAdamThreads, 0, stream>>>(P);
+            if (launch_status() != GQ_OK) return GQ_ERR_CUDA;
         }
-        P.start[P.ndesc] = items;
-        if (items == 0) continue;
-        const int64_t blocks = std::min<int64_t>(items, (int64_t)sm_count() * 32);
-        adamw_kernel<<<(unsigned)blocks, kAdamThreads, 0, stream>>>(P);
-        if (launch_status() != GQ_OK) return GQ_ERR_CUDA;
     }
     return GQ_OK;
 }

@@ -40,7 +40,7 @@ struct AdamDesc {
     int32_t pad;
 };
 
-constexpr int32_t kAdamPBf16 = 1, kAdamGBf16 = 2, kAdamState8 = 4, kAdamVec = 8;
+constexpr int32_t kAdamPBf16 = 1, kAdamGBf16 = 2, kAdamVec = 4;
 
 struct AdamParams {
     int32_t ndesc;
@@ -59,12 +59,21 @@ struct AdamParams {
 
 constexpr uint32_t kAdamStepMul = 0x632BE5ABu, kAdamTensorMul = 0x2C1B3C6Du;
 
-// 32 random bits of an element: two multiply-xorshift rounds.
-__device__ __forceinline__ uint32_t adam_hash(int64_t index, uint32_t key) {
-    uint32_t z = (uint32_t)index * 0x9E3779B9u + (uint32_t)((uint64_t)index >> 32) * 0x7FEB3529u + key;
+// 32 random bits of an element: two multiply-xorshift rounds over a seed that
+// moves by a constant with the index.
+__device__ __forceinline__ uint32_t adam_seed(int64_t index, uint32_t key) {
+    return (uint32_t)index * 0x9E3779B9u + (uint32_t)((uint64_t)index >> 32) * 0x7FEB3529u + key;
+}
+__device__ __forceinline__ uint32_t adam_mix(uint32_t z) {
     z = (z ^ (z >> 16)) * 0x21F0AAADu;
     z = (z ^ (z >> 15)) * 0x735A2D97u;
     return z ^ (z >> 15);
+}
+
+__device__ __forceinline__ float adam_root(float x) {
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // f(q) = RN((q^2)^2); q^2 is exact.
@@ -158,7 +167,9 @@ __device__ __forceinline__ void adam_store8(const uint32_t (&c)[2], void* base, 
     }
 }
 
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamParams P) {
+// S8: the launch's tensors have 8-bit states.
+template <bool S8>
+__global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_constant__ AdamParams P) {
     __shared__ float s_step[3];
     float inv_bc2 = P.inv_bc2, step_size = P.step_size;
     double lr = P.lr;
@@ -201,20 +212,23 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
         if (blk * 256 >= D.numel) continue;                // a whole warp: its block is past the end
         const int n = (int)max((int64_t)0, min((int64_t)8, D.numel - e));
         const bool vec = (D.flags & kAdamVec) && n == 8;
-        const bool pb = D.flags & kAdamPBf16, gb = D.flags & kAdamGBf16, s8 = D.flags & kAdamState8;
+        const bool pb = D.flags & kAdamPBf16, gb = D.flags & kAdamGBf16;
         const float decay = P.d_lr ? (float)(1.0 - lr * D.wd) : D.decay;
         float p[8], g[8], m[8], v[8];
         adam_load(g, D.g, e, n, gb, vec);
         adam_load(p, D.p, e, n, pb, vec);
-        if (s8) {
+        if constexpr (S8) {
             uint32_t cm[2], cv[2];
             adam_load8(cm, D.m, e, n, vec);
             adam_load8(cv, D.v, e, n, vec);
             const float ms = D.ms[blk], vs = D.vs[blk];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                m[i] = __fmul_rn((float)(int8_t)(cm[i >> 2] >> (8 * (i & 3))), ms);
-                v[i] = __fmul_rn(adam_fourth((float)((cv[i >> 2] >> (8 * (i & 3))) & 0xFFu)), vs);
+                // a byte under the exponent of 2^23 less 2^23 is its value, exactly (the signed one offset by 128)
+                const uint32_t bm = __byte_perm(cm[i >> 2] ^ 0x80808080u, 0x4B000000u, 0x7440 + (i & 3));
+                const uint32_t bv = __byte_perm(cv[i >> 2], 0x4B000000u, 0x7440 + (i & 3));
+                m[i] = __fmul_rn(__fsub_rn(__uint_as_float(bm), 8388736.0f), ms);
+                v[i] = __fmul_rn(adam_fourth(__fsub_rn(__uint_as_float(bv), 8388608.0f)), vs);
             }
         } else {
             adam_load(m, D.m, e, n, false, vec);
@@ -231,7 +245,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
         }
         adam_store(p, D.p, e, n, pb, vec);
         if (D.copy) adam_store(p, D.copy, e, n, true, vec);
-        if (!s8) {
+        if constexpr (!S8) {
             adam_store(m, D.m, e, n, false, vec);
             adam_store(v, D.v, e, n, false, vec);
             continue;
@@ -250,30 +264,35 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
         const float im = km ? __fdiv_rn(127.0f, am) : 0.0f;
         const float iv = kv ? __fdiv_rn(4228250625.0f, av) : 0.0f;   // 255^4
         uint32_t cm[2] = {0u, 0u}, cv[2] = {0u, 0u};
+        const uint32_t z0 = adam_seed(e, D.key + key_step);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t z = adam_hash(e + i, D.key + key_step);
-            const float um = __fmul_rn((float)(z >> 16), 1.52587890625e-5f);
-            const float uv = __fmul_rn((float)(z & 0xFFFFu), 1.52587890625e-5f);
-            const float qm = fminf(fmaxf(floorf(__fadd_rn(__fmul_rn(m[i], im), um)), -127.0f), 127.0f);
+            const uint32_t z = adam_mix(z0 + (uint32_t)i * 0x9E3779B9u);   // e is a multiple of 8: no carry into its high word
+            // 16 bits k under the exponent of 1 less 1: k * 2^-16, exactly
+            const float um = __fsub_rn(__uint_as_float((z >> 9 & 0x007FFF80u) | 0x3F800000u), 1.0f);
+            const float uv = __fsub_rn(__uint_as_float((z << 7 & 0x007FFF80u) | 0x3F800000u), 1.0f);
+            // floor by an addition rounded down: the code is in the low byte of the sum's bits
+            const float tm = fminf(fmaxf(__fadd_rn(__fmul_rn(m[i], im), um), -127.0f), 127.0f);
+            const uint32_t qm = __float_as_uint(__fadd_rd(tm, kMagic));
             const float x = __fmul_rn(v[i], iv);
-            // q0: an approximate fourth root, then set right against f itself
-            float q0 = fminf(floorf(__fsqrt_rn(__fsqrt_rn(x))), 254.0f);
-            float f0 = adam_fourth(q0);
+            // q0: an approximate fourth root, at most one off, set right against f itself
+            float q0 = __fsub_rn(__fadd_rd(fminf(adam_root(adam_root(x)), 254.0f), 8388608.0f), 8388608.0f);
+            float f0 = adam_fourth(q0), f1 = adam_fourth(q0 + 1.0f);
             if (f0 > x) {
                 q0 -= 1.0f;
+                f1 = f0;
                 f0 = adam_fourth(q0);
-            }
-            float f1 = adam_fourth(q0 + 1.0f);
-            if (q0 < 254.0f && f1 <= x) {
+            } else if (f1 <= x && q0 < 254.0f) {
                 q0 += 1.0f;
                 f0 = f1;
                 f1 = adam_fourth(q0 + 1.0f);
             }
             float qv = __fmul_rn(uv, __fsub_rn(f1, f0)) < __fsub_rn(x, f0) ? q0 + 1.0f : q0;
-            if (qv == 0.0f && x > 0.0f) qv = 1.0f;
-            cm[i >> 2] |= ((uint32_t)(int)qm & 0xFFu) << (8 * (i & 3));
-            cv[i >> 2] |= ((uint32_t)(int)qv & 0xFFu) << (8 * (i & 3));
+            if (x > 0.0f) qv = fmaxf(qv, 1.0f);
+            const uint32_t bv = __float_as_uint(__fadd_rn(qv, 8388608.0f));
+            const uint32_t sel = (i & 3) == 0 ? 0x3214 : (i & 3) == 1 ? 0x3240 : (i & 3) == 2 ? 0x3410 : 0x4210;
+            cm[i >> 2] = __byte_perm(cm[i >> 2], qm, sel);
+            cv[i >> 2] = __byte_perm(cv[i >> 2], bv, sel);
         }
         adam_store8(cm, D.m, e, n, vec);
         adam_store8(cv, D.v, e, n, vec);

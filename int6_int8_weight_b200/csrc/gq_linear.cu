@@ -57,7 +57,7 @@ gq_status launch(LinParams& P, const void* d_x, int64_t K, int64_t ldx, cudaStre
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * split));
-    cfg.blockDim = dim3(kLinThreads);
+    cfg.blockDim = dim3(S::threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];

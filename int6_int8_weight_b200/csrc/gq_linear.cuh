@@ -291,17 +291,15 @@ __device__ __forceinline__ LinUnit lin_find(const LinParams& P, int tt) {
 //   0       copies: a stage is two column blocks (128 of K): their codes by one
 //           bulk copy, the X tiles by TMA
 //   1       TMEM allocation, then the MMAs
-//   2 .. 17 codes -> bf16 integers in TMEM (A operand): four groups of four
-//           warps, group g takes column block g % 2 of every other stage, thread
-//           r of a group weight row r; then the epilogue
+//   2 ..    codes -> bf16 integers in TMEM (A operand): groups of four warps
+//           that take the stages (or their halves) in turn, thread r of a group
+//           weight row r; then the epilogue
 // Shared memory carries codes and X only, and a code costs about 1.6
 // instructions on the way (masks, shifts, one exact subtraction per pair); the
 // row scale waits until the epilogue.
 // With a split the blocks put their sums into their own shared memory, and
 // after a cluster barrier each finishes its share of the elements, adding the
 // blocks' sums in rank order.
-constexpr int kLinGroups = 4;
-constexpr int kLinThreads = 64 + 128 * kLinGroups;
 constexpr int kLinMaxStages = 8;
 
 template <int QB, int NT>
@@ -311,12 +309,17 @@ struct LinShape {
     static constexpr uint32_t stage = 2 * (x_block + c_block);
     static constexpr uint32_t acc_cols = NT <= 64 ? 64 : NT;
     static constexpr uint32_t slots = (256 - acc_cols) / 64;             // stages of A in TMEM
+    // Conversion groups of four warps, and how many of them share a stage.  Two whole-stage groups wait and hand over
+    // half as often as four half-stage ones (M 16, N = K = 16384: 47.6 us against 51.9); with 128 tokens the MMAs
+    // leave only two slots, and four groups hide more (M 4096, N = K = 8192: 595 us against 736).
+    static constexpr int groups = NT <= 64 ? 2 : 4, parts = NT <= 64 ? 1 : 2;
+    static constexpr int threads = 64 + 128 * groups;
     static constexpr uint32_t bars = 8 * (2 * kLinMaxStages + 2 * 4 + 2) + 64;
     static constexpr int smem(int stages) { return 1024 + stages * (int)stage + (int)bars; }
 };
 
 template <int QB, int NT>
-__global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_constant__ LinParams P) {
+__global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(const __grid_constant__ LinParams P) {
     using S = LinShape<QB, NT>;
     extern __shared__ unsigned char g_smem[];
     __shared__ LinUnit s_unit;
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
             g_bar_init(empty(s), 1);
         }
         for (int t = 0; t < (int)S::slots; ++t) {
-            g_bar_init(wready(t), 8);
+            g_bar_init(wready(t), 4 * S::parts);
             g_bar_init(tfree(t), 1);
         }
         g_bar_init(acc_full, 1);
@@ -432,11 +435,12 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     } else {
         const int grp = (warp - 2) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        constexpr int kStep = kLinGroups / 2;              // stages from one of a group's to its next
+        constexpr int kStep = S::groups / S::parts;       // stages from one of a group's to its next
         static_assert(kStep <= (int)S::slots, "the parity tests below");
-        int s = grp >> 1, t = grp >> 1;
+        const int part = grp % S::parts;
+        int s = grp / S::parts, t = s;
         uint32_t ph = 0u, tph = 0u;
-        for (int i = grp >> 1; i < stages; i += kStep) {
+        for (int i = s; i < stages; i += kStep) {
             // The slot first: once stage i - slots is done, stage i - stages (no later, the ring being at least as deep)
             // has landed, so a parity test of full(s) cannot take an older phase for this one; nor can one of
             // tfree(t), since the group's last stage was at most `slots` before.
@@ -445,11 +449,11 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            if (kb0 + 2 * i + (grp & 1) < kb1) {
-                lin_codes_to_tmem<QB>(c_tile(s, grp & 1) + 16u * r,
-                                      tmem + lanes + S::acc_cols + 64u * t + 32u * (grp & 1));
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            }
+            const uint32_t src = c_tile(s, part) + 16u * r, dst = tmem + lanes + S::acc_cols + 64u * t + 32u * part;
+            const int n = kb1 - kb0 - 2 * i - part;        // blocks from this one on
+            if (n > 0) lin_codes_to_tmem<QB>(src, dst);
+            if (S::parts == 1 && n > 1) lin_codes_to_tmem<QB>(src + S::c_block, dst + 32u);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0) g_arrive(wready(t));
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
         if (!g_wait_warp(acc_full, 0u)) ok = false;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if (stages > 0) {
-            for (int c0 = 8 * grp; c0 < mv; c0 += 8 * kLinGroups) {   // the groups take turns of 8 tokens
+            for (int c0 = 8 * grp; c0 < mv; c0 += 8 * S::groups) {   // the groups take turns of 8 tokens
                 float v[8];
                 lin_tmem_ld8(tmem + lanes + (uint32_t)c0, v);
 #pragma unroll
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     if (split > 1 && mv > 0) {                           // the same in every block of the cluster
         lin_cluster_sync();
         // rows of Y by 128 threads each over the cluster; a thread keeps its column
-        constexpr int kLines = kLinThreads / kLinRows;
+        constexpr int kLines = S::threads / kLinRows;
         const int line = (int)threadIdx.x / kLinRows;
         if (line < kLines && n < P.N)
             for (int c = (int)rank * kLines + line; c < mv; c += (int)split * kLines) {

@@ -20,7 +20,10 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from dataclasses import dataclass
+from itertools import repeat
+from operator import attrgetter
 
 import torch
 
@@ -124,10 +127,9 @@ def _load() -> C.CDLL:
     L.gq_tile_bytes.argtypes = [i64, i64, i32]
     L.gq_tile_bytes.restype = i64
     L.gq_tile_weight.argtypes = [vp, i64, i64, i64, i32, vp, vp]
-    L.gq_gemm_epilogue.argtypes = [vp, i64, i64, i64, vp, vp, i32, i64, C.POINTER(GQEpilogue), vp, i64, vp, vp]
-    L.gq_gemm_grouped.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp, i32, i64, C.POINTER(GQEpilogue), vp, i64, vp,
-                                  vp]
-    L.gq_adamw_step.argtypes = [C.POINTER(GQAdamWTensor), i32, C.POINTER(GQAdamWHyper), vp]
+    L.gq_gemm_epilogue.argtypes = [vp, i64, i64, i64, vp, vp, i32, i64, vp, vp, i64, vp, vp]
+    L.gq_gemm_grouped.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp, i32, i64, vp, vp, i64, vp, vp]
+    L.gq_adamw_step.argtypes = [vp, i32, C.POINTER(GQAdamWHyper), vp]
     for f in ("gq_tile_weight", "gq_gemm_epilogue", "gq_gemm_grouped", "gq_adamw_step"):
         getattr(L, f).restype = i32
     L.gq_test_arm_wait_expiry.argtypes = [i64, C.c_uint64]
@@ -541,20 +543,22 @@ def gemm_fakequant(x: torch.Tensor, w: torch.Tensor, clip: torch.Tensor, qbits: 
     return y
 
 
-def _on(device: torch.device, stream, fn, *args) -> int:
-    """``fn(*args, stream)`` with ``device`` current; its current stream where ``stream`` is None."""
-    if device.type != "cuda":
+def _on(index: int, stream, fn, *args) -> int:
+    """``fn(*args, stream)`` with device ``index`` current; its current stream where ``stream`` is None."""
+    if index < 0:
         raise ValueError("libgq takes CUDA tensors")
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
-    with torch.cuda.device(device):
+    if index == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+    with torch.cuda.device(index):
         return fn(*args, _stream(stream))
 
 
-def _same_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"every tensor of a call lies on one device ({device}, {t.device})")
+_DTYPE_CODES = {torch.float32: GQ_F32, torch.bfloat16: GQ_BF16}
+_ADAMW_TENSOR = struct.Struct("@PPPPPPPqiiiid")              # gq_adamw_tensor
+_numel, _is_contiguous, _get_device = torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.get_device
+_data_ptr, _get_dtype = torch.Tensor.data_ptr, attrgetter("dtype")
+_EPILOGUE = struct.Struct("@PPqiiii")                      # gq_epilogue
+_EPILOGUE_NONE = {(a, y): _EPILOGUE.pack(0, 0, 0, 0, 0, a, y) for a in ACTS.values() for y in (GQ_F32, GQ_BF16)}
 
 
 def tile_weight(packed: torch.Tensor, K: int, qbits: int, stream=None) -> torch.Tensor:
@@ -570,44 +574,74 @@ def tile_weight(packed: torch.Tensor, K: int, qbits: int, stream=None) -> torch.
     E, N = (1, packed.shape[0]) if packed.dim() == 2 else packed.shape[:2]
     nbytes = LIB.gq_tile_bytes(N, K, qbits)
     tiles = torch.empty((nbytes,) if packed.dim() == 2 else (E, nbytes), dtype=torch.uint8, device=packed.device)
-    _check(_on(packed.device, stream, LIB.gq_tile_weight, packed.data_ptr(), E, N, K, qbits, tiles.data_ptr()),
+    _check(_on(packed.get_device(), stream, LIB.gq_tile_weight, packed.data_ptr(), E, N, K, qbits, tiles.data_ptr()),
            "gq_tile_weight")
     return tiles
 
 
+def _rows(t, M, N):
+    """The row pitch of a [M, N] tensor with contiguous rows, or None."""
+    if t.shape != (M, N):
+        return None
+    ld, one = t.stride()
+    if M > 1:
+        return (ld if ld >= N else None) if one == 1 or N <= 1 else None
+    return N if one == 1 or N <= 1 or M == 0 else None
+
+
 def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, out_dtype, stream, check_status):
-    """Argument checks and the call shared by gemm_epilogue and gemm_grouped."""
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or (x.shape[0] and x.stride(1) != 1 and x.shape[1] > 1):
+    """Argument checks and the call shared by gemm_epilogue and gemm_grouped.
+    (Written for few Python operations: a small layer's kernel takes less time than they do.)"""
+    if x.dtype is not torch.bfloat16 or x.dim() != 2 or (ldx := _rows(x, *x.shape)) is None:
         raise ValueError("x must be a bf16 [M, K] tensor with contiguous rows")
     M, K = x.shape
-    lead = scale.shape[:-1]
-    if scale.dtype != torch.float16 or not scale.is_contiguous() or scale.dim() != (2 if offsets is not None else 1):
+    if M <= 1 or K == 0:
+        ldx = -(-K // 8) * 8                               # no second row: any pitch will do
+    shape = scale.shape
+    if scale.dtype is not torch.float16 or len(shape) != (1 if offsets is None else 2) or not scale.is_contiguous():
         raise ValueError("scale_f16 must be a contiguous fp16 tensor, [N] (grouped: [E, N])")
-    N = scale.shape[-1]
-    if tiles.dtype != torch.uint8 or not tiles.is_contiguous() or tiles.shape[:-1] != lead \
-            or tiles.shape[-1] != LIB.gq_tile_bytes(N, K, qbits):
+    N = shape[-1]
+    nbytes = ((N + 127) >> 7) * ((K + 63) >> 6) * (6144 if qbits == 6 else 8192)
+    if qbits not in (6, 8) or tiles.dtype is not torch.uint8 or tiles.shape != (*shape[:-1], nbytes) \
+            or not tiles.is_contiguous():
         raise ValueError("tiles must be what tile_weight gives for these N, K and qbits")
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"act is one of {', '.join(ACTS)}")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=x.device)
-    elif y.shape != (M, N) or (M and y.stride(1) != 1 and N > 1) or (out_dtype is not None and y.dtype != out_dtype):
+        y = x.new_empty((M, N), dtype=out_dtype or torch.bfloat16)
+        ldy = N
+    elif (ldy := _rows(y, M, N)) is None or (out_dtype is not None and y.dtype is not out_dtype):
         raise ValueError("y must be [M, N] with contiguous rows and of out_dtype where that is given")
-    e = GQEpilogue(act=ACTS[act], y_dtype=_dtype_code(y))
-    if bias is not None:
-        if bias.shape != scale.shape or not bias.is_contiguous():
-            raise ValueError("bias must be contiguous, of the shape of scale_f16")
-        e.bias, e.bias_dtype = bias.data_ptr(), _dtype_code(bias)
-    if residual is not None:
-        if residual.shape != (M, N) or (M and residual.stride(1) != 1 and N > 1):
-            raise ValueError("residual must be [M, N] with contiguous rows")
-        e.residual, e.residual_dtype, e.ldr = residual.data_ptr(), _dtype_code(residual), max(residual.stride(0), N)
-    _same_device(x.device, offsets, tiles, scale, bias, residual, y)
-    group = () if offsets is None else (offsets.data_ptr(), scale.shape[0])
+    y_code = _DTYPE_CODES.get(y.dtype)
+    if y_code is None:
+        raise TypeError(f"Y is float32 or bfloat16, got {y.dtype}")
+    dev = x.get_device()
+    same = tiles.get_device() == dev == scale.get_device() == y.get_device()
+    if bias is None and residual is None:
+        epi = _EPILOGUE_NONE[code, y_code]
+    else:
+        b = r = ldr = b_code = r_code = 0
+        if bias is not None:
+            if bias.shape != shape or not bias.is_contiguous():
+                raise ValueError("bias must be contiguous, of the shape of scale_f16")
+            b, b_code = bias.data_ptr(), _dtype_code(bias)
+            same = same and bias.get_device() == dev
+        if residual is not None:
+            ldr = _rows(residual, M, N)
+            if ldr is None:
+                raise ValueError("residual must be [M, N] with contiguous rows")
+            r, r_code = residual.data_ptr(), _dtype_code(residual)
+            same = same and residual.get_device() == dev
+        epi = _EPILOGUE.pack(b, r, ldr, b_code, r_code, code, y_code)
+    if not same or (offsets is not None and offsets.get_device() != dev):
+        raise ValueError("every tensor of a call lies on one device")
     st = torch.empty(1, dtype=torch.int32, device=x.device) if check_status else None
-    _check(_on(x.device, stream, fn, x.data_ptr(), M, K, max(x.stride(0), K) if M > 1 else -(-K // 8) * 8, *group,
-               tiles.data_ptr(), scale.data_ptr(), qbits, N, C.byref(e), y.data_ptr(),
-               max(y.stride(0), N) if M > 1 else N, _ptr(st) or None), where)
+    group = () if offsets is None else (offsets.data_ptr(), shape[0])
+    status = _on(dev, stream, fn, x.data_ptr(), M, K, ldx, *group, tiles.data_ptr(), scale.data_ptr(), qbits, N, epi,
+                 y.data_ptr(), ldy, None if st is None else st.data_ptr())
+    if status:
+        _check(status, where)
     if check_status and (v := int(st.item())):
         raise GQError(0, where, f"device status {v:#x}")
     return y
@@ -658,54 +692,61 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     ``grad_scale``: fp32 device tensor that multiplies every gradient.  ``seed``
     is that of the 8-bit states' rounding."""
     n = len(params)
-    if not (len(grads) == len(exp_avgs) == len(exp_avg_sqs) == n) or (copies is not None and len(copies) != n) \
-            or (scales is not None and (len(scales) != 2 or len(scales[0]) != n or len(scales[1]) != n)):
-        raise ValueError("params, grads, states, scales and copies are lists of one length")
-    if n == 0:
+    if n == 0 and not (len(grads) or len(exp_avgs) or len(exp_avg_sqs)):
         return
-    wds = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else weight_decay
-    if len(wds) != n:
-        raise ValueError("weight_decay is a number or one per tensor")
-    dev = params[0].device
-    arr = (GQAdamWTensor * n)()
-    for i, (p, g, m, v) in enumerate(zip(params, grads, exp_avgs, exp_avg_sqs)):
-        numel = p.numel()
-        bits = 32 if scales is None else 8
-        want = (torch.float32, torch.float32) if bits == 32 else (torch.int8, torch.uint8)
-        if (m.dtype, v.dtype) != want:
-            raise TypeError("states are fp32, or int8 / uint8 codes with scales")
-        if not (g.numel() == m.numel() == v.numel() == numel) \
-                or not (p.is_contiguous() and g.is_contiguous() and m.is_contiguous() and v.is_contiguous()):
-            raise ValueError("weights, gradients and states are contiguous and of one size")
-        if not (p.device == g.device == m.device == v.device == dev):
+    # whole lists at a time: a loop over the tensors would take longer than the step of a small model
+    bits = 32 if scales is None else 8
+    lists = [params, grads, exp_avgs, exp_avg_sqs]
+    if bits == 8:
+        lists += scales
+    if len(lists) not in (4, 6) or any(len(ts) != n for ts in lists) or (copies is not None and len(copies) != n):
+        raise ValueError("params, grads, states, scales and copies are lists of one length")
+    numel = list(map(_numel, params))
+    dev = params[0].get_device()
+    for ts in lists:
+        if not all(map(_is_contiguous, ts)):
+            raise ValueError("weights, gradients, states and scales are contiguous")
+        if set(map(_get_device, ts)) != {dev}:
             raise ValueError("every tensor of a call lies on one device")
-        t = arr[i]
-        t.p, t.g, t.m, t.v, t.numel = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), numel
-        t.p_dtype, t.g_dtype, t.state_bits, t.weight_decay = _dtype_code(p), _dtype_code(g), bits, wds[i]
-        if bits == 8:
-            ms, vs = scales[0][i], scales[1][i]
-            if ms.dtype != torch.float32 or vs.dtype != torch.float32 or not ms.is_contiguous() \
-                    or not vs.is_contiguous() or not (ms.numel() == vs.numel() == -(-numel // ADAMW_BLOCK)):
-                raise ValueError("scales are contiguous fp32 tensors of ceil(numel / 256) elements")
-            _same_device(dev, ms, vs)
-            t.m_scale, t.v_scale = ms.data_ptr(), vs.data_ptr()
-        if copies is not None and copies[i] is not None:
-            c = copies[i]
-            if c.dtype != torch.bfloat16 or c.numel() != numel or not c.is_contiguous():
+    for ts in lists[1:4]:
+        if list(map(_numel, ts)) != numel:
+            raise ValueError("weights, gradients and states are of one size")
+    try:
+        p_codes, g_codes = ([_DTYPE_CODES[k] for k in map(_get_dtype, ts)] for ts in (params, grads))
+    except KeyError as e:
+        raise TypeError(f"weights and gradients are float32 or bfloat16, got {e.args[0]}") from None
+    if set(map(_get_dtype, exp_avgs)) != {torch.float32 if bits == 32 else torch.int8} \
+            or set(map(_get_dtype, exp_avg_sqs)) != {torch.float32 if bits == 32 else torch.uint8}:
+        raise TypeError("states are fp32, or int8 / uint8 codes with scales")
+    if bits == 8:
+        blocks = [-(-k // ADAMW_BLOCK) for k in numel]
+        if any(list(map(_numel, ts)) != blocks or set(map(_get_dtype, ts)) != {torch.float32} for ts in scales):
+            raise ValueError("scales are contiguous fp32 tensors of ceil(numel / 256) elements")
+    copy = repeat(0)
+    if copies is not None:
+        for c, k in zip(copies, numel):
+            if c is not None and (c.dtype is not torch.bfloat16 or c.numel() != k or not c.is_contiguous()
+                                  or c.get_device() != dev):
                 raise ValueError("copies are contiguous bf16 tensors of the weights' sizes")
-            _same_device(dev, c)
-            t.p_copy = c.data_ptr()
+        copy = map(_ptr, copies)
+    one = isinstance(weight_decay, (int, float))
+    if not one and len(weight_decay) != n:
+        raise ValueError("weight_decay is a number or one per tensor")
+    pointers = [map(_data_ptr, ts) for ts in lists] + [repeat(0)] * (6 - len(lists))
+    desc = b"".join(map(_ADAMW_TENSOR.pack, *pointers, copy, numel, p_codes, g_codes, repeat(bits), repeat(0),
+                        repeat(weight_decay) if one else weight_decay))
     h = GQAdamWHyper(beta1=betas[0], beta2=betas[1], eps=eps, seed=seed & 0xFFFFFFFF)
     for name, value, dtype in (("step", step, torch.int64), ("lr", lr, torch.float32),
                                ("grad_scale", grad_scale, torch.float32)):
         if isinstance(value, torch.Tensor):
             if value.dtype != dtype or value.numel() != 1:
                 raise ValueError(f"{name} on the device is one {dtype} element")
-            _same_device(dev, value)
+            if value.get_device() != dev:
+                raise ValueError("every tensor of a call lies on one device")
             setattr(h, "d_" + name, value.data_ptr())
         elif value is not None:
             setattr(h, name, value)
-    _check(_on(dev, stream, LIB.gq_adamw_step, arr, n, C.byref(h)), "gq_adamw_step")
+    _check(_on(dev, stream, LIB.gq_adamw_step, desc, n, C.byref(h)), "gq_adamw_step")
 
 
 def ste_bwd(g_out: torch.Tensor, g_w: torch.Tensor | None = None, stream=None) -> torch.Tensor:
