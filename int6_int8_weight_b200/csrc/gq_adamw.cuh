@@ -50,6 +50,7 @@ struct AdamParams {
     float b1, c1, b2, c2, eps;
     float inv_bc2;        // RN(1 / sqrt(1 - b2^t))
     float step_size;      // RN(lr / (1 - b1^t))
+    float one;            // 1
     const int64_t* d_step;
     const float* d_lr;
     const float* d_grad_scale;
@@ -72,14 +73,45 @@ __device__ __forceinline__ uint32_t adam_mix(uint32_t z) {
 
 __device__ __forceinline__ float adam_root(float x) {
     float r;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
+// Two elements in one register pair: a pair costs one instruction issue, which
+// is what bounds the 8-bit step.  Every operation is one rounding.  The code
+// generator fuses a paired product into a paired sum even where contraction is
+// off, so a sum is written x * one + y with a 1 that it cannot see (a kernel
+// parameter): a product times an unknown number has nothing to be fused with.
+using AdamF2 = uint64_t;
+__device__ __forceinline__ AdamF2 adam2(float lo, float hi) {
+    AdamF2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ AdamF2 adam2(float x) { return adam2(x, x); }
+__device__ __forceinline__ void adam2_out(AdamF2 a, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a));
+}
+__device__ __forceinline__ AdamF2 adam2_fma(AdamF2 a, AdamF2 b, AdamF2 c) {
+    AdamF2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ AdamF2 adam2_mul(AdamF2 a, AdamF2 b) { return adam2_fma(a, b, adam2(-0.0f)); }
+struct AdamOne {
+    AdamF2 one, minus;           // (1, 1) and (-1, -1)
+    __device__ __forceinline__ AdamF2 add(AdamF2 a, AdamF2 b) const { return adam2_fma(a, one, b); }
+    __device__ __forceinline__ AdamF2 sub(AdamF2 a, AdamF2 b) const { return adam2_fma(b, minus, a); }
+    __device__ __forceinline__ AdamF2 add_down(AdamF2 a, AdamF2 b) const {   // rounded down
+        AdamF2 r;
+        asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(one), "l"(b));
+        return r;
+    }
+};
 // f(q) = RN((q^2)^2); q^2 is exact.
-__device__ __forceinline__ float adam_fourth(float q) {
-    const float t = __fmul_rn(q, q);
-    return __fmul_rn(t, t);
+__device__ __forceinline__ AdamF2 adam2_fourth(AdamF2 q) {
+    const AdamF2 t = adam2_mul(q, q);
+    return adam2_mul(t, t);
 }
 
 // 8 consecutive elements of a float / bf16 array as floats (vector path:
@@ -169,7 +201,7 @@ __device__ __forceinline__ void adam_store8(const uint32_t (&c)[2], void* base, 
 
 // S8: the launch's tensors have 8-bit states.
 template <bool S8>
-__global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_constant__ AdamParams P) {
+__global__ void __launch_bounds__(kAdamThreads, S8 ? 5 : 4) adamw_kernel(const __grid_constant__ AdamParams P) {
     __shared__ float s_step[3];
     float inv_bc2 = P.inv_bc2, step_size = P.step_size;
     double lr = P.lr;
@@ -196,6 +228,7 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_con
         key_step = __float_as_uint(s_step[2]);
         if (P.d_lr) lr = (double)*P.d_lr;
     }
+    const AdamOne U{adam2(P.one), adam2(-P.one)};
     const float gs = P.d_grad_scale ? *P.d_grad_scale : 1.0f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t total = P.start[P.ndesc];
@@ -222,26 +255,36 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_con
             adam_load8(cm, D.m, e, n, vec);
             adam_load8(cv, D.v, e, n, vec);
             const float ms = D.ms[blk], vs = D.vs[blk];
+            // a byte under the exponent of 2^23 less 2^23 is its value, exactly (the signed one offset by 128)
+            auto bytes = [&](uint32_t c, int i) {
+                return adam2(__uint_as_float(__byte_perm(c, 0x4B000000u, 0x7440 + i)),
+                             __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7441 + i)));
+            };
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // a byte under the exponent of 2^23 less 2^23 is its value, exactly (the signed one offset by 128)
-                const uint32_t bm = __byte_perm(cm[i >> 2] ^ 0x80808080u, 0x4B000000u, 0x7440 + (i & 3));
-                const uint32_t bv = __byte_perm(cv[i >> 2], 0x4B000000u, 0x7440 + (i & 3));
-                m[i] = __fmul_rn(__fsub_rn(__uint_as_float(bm), 8388736.0f), ms);
-                v[i] = __fmul_rn(adam_fourth(__fsub_rn(__uint_as_float(bv), 8388608.0f)), vs);
+            for (int i = 0; i < 8; i += 2) {
+                const AdamF2 qm = U.add(bytes(cm[i >> 2] ^ 0x80808080u, i & 3), adam2(-8388736.0f));
+                const AdamF2 qv = U.add(bytes(cv[i >> 2], i & 3), adam2(-8388608.0f));
+                adam2_out(adam2_mul(qm, adam2(ms)), m[i], m[i + 1]);
+                adam2_out(adam2_mul(adam2_fourth(qv), adam2(vs)), v[i], v[i + 1]);
             }
         } else {
             adam_load(m, D.m, e, n, false, vec);
             adam_load(v, D.v, e, n, false, vec);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float gi = P.d_grad_scale ? __fmul_rn(g[i], gs) : g[i];
-            m[i] = __fadd_rn(__fmul_rn(m[i], P.b1), __fmul_rn(gi, P.c1));
-            v[i] = __fadd_rn(__fmul_rn(v[i], P.b2), __fmul_rn(__fmul_rn(gi, gi), P.c2));
-            const float d = __fadd_rn(__fmul_rn(__fsqrt_rn(v[i]), inv_bc2), P.eps);
-            const float u = __fmul_rn(__fdiv_rn(m[i], d), step_size);
-            p[i] = __fsub_rn(__fmul_rn(p[i], decay), u);
+        for (int i = 0; i < 8; i += 2) {
+            AdamF2 g2 = adam2(g[i], g[i + 1]);
+            if (P.d_grad_scale) g2 = adam2_mul(g2, adam2(gs));
+            const AdamF2 m2 = U.add(adam2_mul(adam2(m[i], m[i + 1]), adam2(P.b1)), adam2_mul(g2, adam2(P.c1)));
+            const AdamF2 v2 = U.add(adam2_mul(adam2(v[i], v[i + 1]), adam2(P.b2)),
+                                    adam2_mul(adam2_mul(g2, g2), adam2(P.c2)));
+            adam2_out(m2, m[i], m[i + 1]);
+            adam2_out(v2, v[i], v[i + 1]);
+            const AdamF2 r2 = adam2(__fsqrt_rn(v[i]), __fsqrt_rn(v[i + 1]));
+            float d0, d1;
+            adam2_out(U.add(adam2_mul(r2, adam2(inv_bc2)), adam2(P.eps)), d0, d1);
+            const AdamF2 u2 = adam2_mul(adam2(__fdiv_rn(m[i], d0), __fdiv_rn(m[i + 1], d1)), adam2(step_size));
+            adam2_out(U.sub(adam2_mul(adam2(p[i], p[i + 1]), adam2(decay)), u2), p[i], p[i + 1]);
         }
         adam_store(p, D.p, e, n, pb, vec);
         if (D.copy) adam_store(p, D.copy, e, n, true, vec);
@@ -266,33 +309,49 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_con
         uint32_t cm[2] = {0u, 0u}, cv[2] = {0u, 0u};
         const uint32_t z0 = adam_seed(e, D.key + key_step);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t z = adam_mix(z0 + (uint32_t)i * 0x9E3779B9u);   // e is a multiple of 8: no carry into its high word
-            // 16 bits k under the exponent of 1 less 1: k * 2^-16, exactly
-            const float um = __fsub_rn(__uint_as_float((z >> 9 & 0x007FFF80u) | 0x3F800000u), 1.0f);
-            const float uv = __fsub_rn(__uint_as_float((z << 7 & 0x007FFF80u) | 0x3F800000u), 1.0f);
-            // floor by an addition rounded down: the code is in the low byte of the sum's bits
-            const float tm = fminf(fmaxf(__fadd_rn(__fmul_rn(m[i], im), um), -127.0f), 127.0f);
-            const uint32_t qm = __float_as_uint(__fadd_rd(tm, kMagic));
-            const float x = __fmul_rn(v[i], iv);
-            // q0: an approximate fourth root, at most one off, set right against f itself
-            float q0 = __fsub_rn(__fadd_rd(fminf(adam_root(adam_root(x)), 254.0f), 8388608.0f), 8388608.0f);
-            float f0 = adam_fourth(q0), f1 = adam_fourth(q0 + 1.0f);
-            if (f0 > x) {
-                q0 -= 1.0f;
-                f1 = f0;
-                f0 = adam_fourth(q0);
-            } else if (f1 <= x && q0 < 254.0f) {
-                q0 += 1.0f;
-                f0 = f1;
-                f1 = adam_fourth(q0 + 1.0f);
+        for (int i = 0; i < 8; i += 2) {
+            // e is a multiple of 8: no carry into the index's high word
+            const uint32_t za = adam_mix(z0 + (uint32_t)i * 0x9E3779B9u), zb = adam_mix(z0 + (uint32_t)(i + 1) * 0x9E3779B9u);
+            // 16 bits k under the exponent of 2^23: (2^23 + k) * 2^-16 - 2^7 = k * 2^-16, exactly
+            auto unit = [](uint32_t a, uint32_t b, uint32_t half) {
+                return adam2_fma(adam2(__uint_as_float(__byte_perm(a, 0x4B000000u, half)),
+                                       __uint_as_float(__byte_perm(b, 0x4B000000u, half))),
+                                 adam2(1.52587890625e-5f), adam2(-128.0f));
+            };
+            const AdamF2 um = unit(za, zb, 0x7432), uv = unit(za, zb, 0x7410);
+            // floor by an addition rounded down: the code is in the low byte of the sum's bits (it is at most 127:
+            // m' * RN(127 / a) is below 127 + 2^-15, and u at most 1 - 2^-16)
+            float t0, t1;
+            adam2_out(U.add(adam2_mul(adam2(m[i], m[i + 1]), adam2(im)), um), t0, t1);
+            adam2_out(U.add_down(adam2(fmaxf(t0, -127.0f), fmaxf(t1, -127.0f)), adam2(kMagic)), t0, t1);
+            const AdamF2 x = adam2_mul(adam2(v[i], v[i + 1]), adam2(iv));
+            float x0, x1, q0, q1, f0, f1;
+            adam2_out(x, x0, x1);
+            // q0: a fourth root good to 2^-20, raised by 2^-18, so that its floor is never too small and at most one too
+            // large; set right against f itself.  qi = q + 2^23: the code in the low byte.
+            adam2_out(adam2_mul(adam2(adam_root(adam_root(x0)), adam_root(adam_root(x1))), adam2(1.000003814697265625f)),
+                      q0, q1);
+            AdamF2 qi = U.add_down(adam2(fminf(q0, 254.0f), fminf(q1, 254.0f)), adam2(8388608.0f));
+            AdamF2 q = U.add(qi, adam2(-8388608.0f));
+            AdamF2 f = adam2_fourth(q);
+            adam2_out(f, f0, f1);
+            if (f0 > x0 || f1 > x1) {
+                adam2_out(q, q0, q1);
+                q = adam2(f0 > x0 ? q0 - 1.0f : q0, f1 > x1 ? q1 - 1.0f : q1);
+                qi = U.add(q, adam2(8388608.0f));
+                f = adam2_fourth(q);
             }
-            float qv = __fmul_rn(uv, __fsub_rn(f1, f0)) < __fsub_rn(x, f0) ? q0 + 1.0f : q0;
-            if (x > 0.0f) qv = fmaxf(qv, 1.0f);
-            const uint32_t bv = __float_as_uint(__fadd_rn(qv, 8388608.0f));
-            const uint32_t sel = (i & 3) == 0 ? 0x3214 : (i & 3) == 1 ? 0x3240 : (i & 3) == 2 ? 0x3410 : 0x4210;
-            cm[i >> 2] = __byte_perm(cm[i >> 2], qm, sel);
-            cv[i >> 2] = __byte_perm(cv[i >> 2], bv, sel);
+            // one more where u (f(q + 1) - f(q)) < x - f(q); at q = 0 where 0 < x
+            float s0, s1, r0, r1;
+            adam2_out(q, q0, q1);
+            adam2_out(adam2_mul(adam2_mul(uv, U.sub(adam2_fourth(U.add(q, U.one)), f)),
+                                adam2(fminf(q0, 1.0f), fminf(q1, 1.0f))), s0, s1);
+            adam2_out(U.sub(x, f), r0, r1);
+            adam2_out(U.add(qi, adam2(s0 < r0 ? 1.0f : 0.0f, s1 < r1 ? 1.0f : 0.0f)), q0, q1);
+            // two code bytes into their word
+            const uint32_t sel = (i & 2) ? 0x5410u : 0x3254u;
+            cm[i >> 2] = __byte_perm(cm[i >> 2], __byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x0040), sel);
+            cv[i >> 2] = __byte_perm(cv[i >> 2], __byte_perm(__float_as_uint(q0), __float_as_uint(q1), 0x0040), sel);
         }
         adam_store8(cm, D.m, e, n, vec);
         adam_store8(cv, D.v, e, n, vec);
