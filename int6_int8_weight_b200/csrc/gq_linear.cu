@@ -2,6 +2,7 @@
 // gq_gemm_grouped (include/gq.h): argument checks, launch planning, launches.
 #include <algorithm>
 #include <atomic>
+#include <cstdlib>
 #include <cstring>
 
 #include "gq_host.h"
@@ -68,6 +69,38 @@ gq_status launch(LinParams& P, const void* d_x, int64_t K, int64_t ldx, cudaStre
     return cuda_status(cudaLaunchKernelEx(&cfg, linear_kernel<QB, NT>, static_cast<const LinParams&>(P)));
 }
 
+// Whether the pair kernel is the faster one.
+bool pair_pays(const LinParams& P) {
+    const char* f = getenv("LIN_PAIR");
+    if (f) return f[0] == '1';
+    return P.M / P.E >= 192;
+}
+
+// The kernel of 256 x 256 tiles over pairs of SMs.
+template <int QB>
+gq_status launch_pair(LinParams& P, const void* d_x, int64_t K, int64_t ldx, cudaStream_t stream) {
+    using S = PairShape<QB>;
+    static std::atomic<bool> set[kMaxDevices];
+    if (!map_x(&P.tmap_x, d_x, P.M, K, ldx, kPairNT / 2)) return GQ_ERR_UNSUPPORTED;
+    constexpr int smem = S::smem(S::stages);
+    int dev = 0;
+    if (cuda_status(cudaGetDevice(&dev)) != GQ_OK) return GQ_ERR_CUDA;
+    if (dev >= kMaxDevices || !set[dev].load(std::memory_order_relaxed)) {
+        if (cuda_status(cudaFuncSetAttribute(linear_pair_kernel<QB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             smem)) != GQ_OK)
+            return GQ_ERR_CUDA;
+        if (dev < kMaxDevices) set[dev].store(true, std::memory_order_relaxed);
+    }
+    // as many pairs as have work (for experts, at most); 32-bit unit numbers
+    const int64_t tts = P.offsets ? P.M / kPairNT + std::min<int64_t>(P.E, P.M) : (P.M + kPairNT - 1) / kPairNT;
+    const int64_t units = tts * ((P.rts + 1) / 2);
+    if (units > INT32_MAX / 2) return GQ_ERR_UNSUPPORTED;
+    const int64_t pairs = std::min<int64_t>(units, sm_count() / 2);
+    if ((units / pairs + 1) * ((P.kbs + 1) / 2) > INT32_MAX / 2) return GQ_ERR_UNSUPPORTED;   // stages are counted in 32 bits
+    linear_pair_kernel<QB><<<(unsigned)(2 * pairs), kPairThreads, smem, stream>>>(P);
+    return launch_status();
+}
+
 gq_status linear(const void* d_x, int64_t M, int64_t K, int64_t ldx, const int32_t* d_offsets, int64_t E,
                  const uint8_t* d_tiles, const uint16_t* d_scale_f16, int qbits, int64_t N, const gq_epilogue* epi,
                  void* d_y, int64_t ldy, int32_t* d_status, cudaStream_t stream) {
@@ -112,6 +145,7 @@ gq_status linear(const void* d_x, int64_t M, int64_t K, int64_t ldx, const int32
         linear_empty_kernel<<<(unsigned)std::min<int64_t>(M, 65535), 256, 0, stream>>>(P);
         return launch_status();
     }
+    if (pair_pays(P)) return qbits == 6 ? launch_pair<6>(P, d_x, K, ldx, stream) : launch_pair<8>(P, d_x, K, ldx, stream);
     // tokens of a tile: the rows an expert has on average, rounded up to 16 .. 128
     const int64_t rows = (M + E - 1) / E;
     const int nt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;

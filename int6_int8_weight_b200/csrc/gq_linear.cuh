@@ -120,15 +120,25 @@ struct LinEpi {
     int32_t bias_bf16, residual_bf16, y_bf16, act;
 };
 
-__device__ __forceinline__ float lin_act(float z, int act) {
-    switch (act) {
-        case GQ_ACT_RELU: return z < 0.0f ? 0.0f : z;      // NaN stays
-        case GQ_ACT_RELU2: z = z < 0.0f ? 0.0f : z; return z * z;
-        case GQ_ACT_LEAKY_RELU2: z = z < 0.0f ? 0.5f * z : z; return z * z;
-        case GQ_ACT_SILU: return z / (1.0f + expf(-z));
-        case GQ_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-        case GQ_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-        default: return z;
+// N values through the activation, in place.  silu and the tanh form of gelu
+// (z * sigmoid(2 w)) take the exponential and the quotient from the special
+// function unit: a few units in the last place of a factor at most 1.  NaN
+// stays NaN.
+template <int N>
+__device__ __forceinline__ void lin_act(float (&z)[N], int act) {
+    if (act == GQ_ACT_NONE) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float x = z[i];
+        if (act <= GQ_ACT_LEAKY_RELU2) {
+            const float r = x < 0.0f ? (act == GQ_ACT_LEAKY_RELU2 ? 0.5f * x : 0.0f) : x;
+            z[i] = act == GQ_ACT_RELU ? r : r * r;
+        } else if (act == GQ_ACT_GELU) {
+            z[i] = 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+        } else {
+            const float w = act == GQ_ACT_SILU ? x : 1.5957691216057308f * __fmaf_rn(0.044715f * x, x * x, x);
+            z[i] = __fdividef(x, 1.0f + __expf(-w));
+        }
     }
 }
 
@@ -136,14 +146,39 @@ __device__ __forceinline__ float lin_elem(const void* p, int64_t i, int bf16) {
     return bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
-// Y[m, n] from the sum, the row's scale and bias.
-__device__ __forceinline__ void lin_finish(const LinEpi& E, float acc, float s, float b, int64_t m, int64_t n) {
-    float z = acc * s;
-    if (E.bias) z += b;
-    float y = lin_act(z, E.act);
-    if (E.residual) y += lin_elem(E.residual, m * E.ldr + n, E.residual_bf16);
-    if (E.y_bf16) static_cast<uint16_t*>(E.y)[m * E.ldy + n] = float_to_bf16_bits(y);
-    else static_cast<float*>(E.y)[m * E.ldy + n] = y;
+// The first `count` of N rows of Y from row m on, column n, from their sums, the
+// column's scale and bias.  The residual is read before anything is written:
+// it may be Y itself, and N loads are in flight at once.
+template <int N>
+__device__ __forceinline__ void lin_finish(const LinEpi& E, float (&v)[N], int count, float s, float b, int64_t m,
+                                           int64_t n) {
+    float r[N];
+    if (E.residual) {
+        const char* p = static_cast<const char*>(E.residual) + (m * E.ldr + n) * (E.residual_bf16 ? 2 : 4);
+        const int64_t step = E.ldr * (E.residual_bf16 ? 2 : 4);
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += step)
+            r[i] = i >= count ? 0.0f : lin_elem(p, 0, E.residual_bf16);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= s;
+    if (E.bias) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += b;
+    }
+    lin_act(v, E.act);
+    if (E.residual) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += r[i];
+    }
+    char* p = static_cast<char*>(E.y) + (m * E.ldy + n) * (E.y_bf16 ? 2 : 4);
+    const int64_t step = E.ldy * (E.y_bf16 ? 2 : 4);
+#pragma unroll
+    for (int i = 0; i < N; ++i, p += step) {
+        if (i >= count) break;
+        if (E.y_bf16) *reinterpret_cast<uint16_t*>(p) = float_to_bf16_bits(v[i]);
+        else *reinterpret_cast<float*>(p) = v[i];
+    }
 }
 
 struct LinParams {
@@ -177,6 +212,24 @@ __device__ __forceinline__ void lin_tmem_ld8(uint32_t taddr, float (&f)[8]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]);
+}
+
+// Columns taddr + 64 j .. + 15 (j = 0 .. 3) of this thread's lane into 64
+// registers; one asm block, so that nothing touches them before they are there.
+__device__ __forceinline__ void lin_tmem_drain(uint32_t taddr, float (&v)[16][4]) {
+#define GQ_LD16 "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+#define GQ_OUT4(j) "=f"(v[j][0]), "=f"(v[j][1]), "=f"(v[j][2]), "=f"(v[j][3])
+    asm volatile(GQ_LD16 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%64];\n\t"
+                 GQ_LD16 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%65];\n\t"
+                 GQ_LD16 "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, [%66];\n\t"
+                 GQ_LD16 "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%67];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : GQ_OUT4(0), GQ_OUT4(1), GQ_OUT4(2), GQ_OUT4(3), GQ_OUT4(4), GQ_OUT4(5), GQ_OUT4(6), GQ_OUT4(7),
+                   GQ_OUT4(8), GQ_OUT4(9), GQ_OUT4(10), GQ_OUT4(11), GQ_OUT4(12), GQ_OUT4(13), GQ_OUT4(14), GQ_OUT4(15)
+                 : "r"(taddr), "r"(taddr + 64u), "r"(taddr + 128u), "r"(taddr + 192u)
+                 : "memory");
+#undef GQ_LD16
+#undef GQ_OUT4
 }
 
 // The binary32 at shared address `addr` of block `rank` of the cluster.
@@ -236,6 +289,34 @@ struct LinUnit {
     int32_t bad;                 // an offset out of order or range was met
 };
 
+// Tile j of the rows [a, b): as few tiles as NT allows, of even size (a multiple
+// of 32, the granularity of the pair kernel's MMAs).
+template <int NT>
+__device__ __forceinline__ void lin_cut(LinUnit& u, int a, int b, int j) {
+    const unsigned rows = (unsigned)(b - a), n = (rows + NT - 1u) / NT;
+    const int step = NT < 32 ? NT : (int)((rows + n - 1u) / n + 31u & ~31u);
+    u.m0 = a + j * step;
+    u.m1 = min(b - u.m0, step) + u.m0;
+}
+
+// Token tiles of the whole batch (one warp).
+template <int NT>
+__device__ __forceinline__ int lin_total(const LinParams& P) {
+    if (!P.offsets) return (int)((P.M + NT - 1) / NT);
+    unsigned sum = 0;
+    for (int e = threadIdx.x & 31; e < (int)P.E; e += 32) {
+        const int p = __ldg(P.offsets + e), q = __ldg(P.offsets + e + 1);
+        if (p >= 0 && q >= p && q <= (int)P.M)
+            sum += ((unsigned)(q - p) + NT - 1u) / NT;
+        else if (P.status)
+            atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x8u);
+    }
+    return (int)__reduce_add_sync(0xffffffffu, sum);
+}
+
+// The MMAs' N for a unit of the pair kernel: its rows in steps of 32.
+__device__ __forceinline__ int lin_cols(const LinUnit& u) { return u.m1 - u.m0 + 31 & ~31; }
+
 // Unit `tt` of the token tiles (expert-major) found by one warp: every lane
 // scans its share of the experts' tile counts.  m0 = m1 past the last.
 template <int NT>
@@ -243,8 +324,7 @@ __device__ __forceinline__ LinUnit lin_find(const LinParams& P, int tt) {
     LinUnit u{0, 0, 0, 0, 0};
     const int M = (int)P.M;
     if (!P.offsets) {
-        u.m0 = tt * NT;
-        u.m1 = min(M - u.m0, NT) + u.m0;
+        lin_cut<NT>(u, 0, M, tt);
         return u;
     }
     const int lane = threadIdx.x & 31;
@@ -273,8 +353,8 @@ __device__ __forceinline__ LinUnit lin_find(const LinParams& P, int tt) {
         if (who && u.m1 == 0) {
             const int l = __ffs(who) - 1;
             u.e = e0 + l;
-            u.m0 = __shfl_sync(0xffffffffu, a + (tt - (at - n)) * NT, l);
-            u.m1 = min(__shfl_sync(0xffffffffu, b, l) - u.m0, NT) + u.m0;
+            lin_cut<NT>(u, __shfl_sync(0xffffffffu, a, l), __shfl_sync(0xffffffffu, b, l),
+                        __shfl_sync(0xffffffffu, tt - (at - n), l));
             if (blockIdx.x != 0) return u;                 // block 0 reads on: every offset is checked
         }
         before = __shfl_sync(0xffffffffu, at, 31);
@@ -472,15 +552,16 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
             for (int c0 = 8 * grp; c0 < mv; c0 += 8 * S::groups) {   // the groups take turns of 8 tokens
                 float v[8];
                 lin_tmem_ld8(tmem + lanes + (uint32_t)c0, v);
+                if (split > 1) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (c0 + i >= mv) break;
-                    if (split > 1)
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + 4u * (uint32_t)((c0 + i) * kLinRows + r)),
-                                     "f"(v[i])
-                                     : "memory");
-                    else if (n < P.N)
-                        lin_finish(P.epi, v[i], sc, bi, (int64_t)u.m0 + c0 + i, n);
+                    for (int i = 0; i < 8; ++i)
+                        if (c0 + i < mv)
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(
+                                             base + 4u * (uint32_t)((c0 + i) * kLinRows + r)),
+                                         "f"(v[i])
+                                         : "memory");
+                } else if (n < P.N) {
+                    lin_finish(P.epi, v, mv - c0, sc, bi, (int64_t)u.m0 + c0, n);
                 }
             }
         }
@@ -495,9 +576,9 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
         if (line < kLines && n < P.N)
             for (int c = (int)rank * kLines + line; c < mv; c += (int)split * kLines) {
                 const uint32_t at = base + 4u * (uint32_t)(c * kLinRows + ((int)threadIdx.x & 127));
-                float v = 0.0f;
-                for (int q = 0; q < (int)split; ++q) v += lin_ld_peer(at, (uint32_t)q);
-                lin_finish(P.epi, v, sc, bi, (int64_t)u.m0 + c, n);
+                float v[1] = {0.0f};
+                for (int q = 0; q < (int)split; ++q) v[0] += lin_ld_peer(at, (uint32_t)q);
+                lin_finish(P.epi, v, 1, sc, bi, (int64_t)u.m0 + c, n);
             }
         lin_cluster_sync();                                // its memory is read until here
     }
@@ -506,6 +587,280 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
     if (warp == 1) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ------------------------------------------------------------ pair kernel --
+//
+// Many rows: two blocks of a cluster (on two SMs) work on one tile of 256
+// weight rows by up to 256 rows of X with cta_group::2 MMAs (M = 256).  Each
+// converts its own 128 weight rows into its own tensor memory and loads half of
+// the X tile; the MMAs, issued by block 0, read both halves.  So a code is
+// converted once per 256 tokens and X crosses to each SM half as often as with
+// one block per tile: per SM and column block 16 KB of X and 6 KB of codes
+// against 512 cycles of MMAs.
+// Persistent: a pair takes every pairs-th unit.  TMEM: 256 columns of sums, 256
+// for four stages of A.  The conversion warps run ahead into the next unit by
+// those four stages (2048 cycles of MMAs), then drain the finished sums into
+// registers (which frees them for the next unit's MMAs), and only then apply the
+// epilogue and store, while the MMAs run on what was converted ahead.
+// Block 0's barriers gather both blocks' conversions (wready) and drains
+// (acc_empty); the MMAs' commits arrive on both blocks' barriers.
+constexpr int kPairNT = 256;
+constexpr int kPairThreads = 64 + 512;
+constexpr int kPairSlots = 4;
+constexpr int kPairMaxStages = 5;
+
+template <int QB>
+struct PairShape {
+    static constexpr uint32_t x_block = kPairNT / 2 * 128u;              // half a tile's column block of X
+    static constexpr uint32_t c_block = lin_block_bytes(QB);
+    static constexpr uint32_t stage = 2 * (x_block + c_block);
+    static constexpr uint32_t bars = 8 * (2 * kPairMaxStages + 2 * kPairSlots + 2) + 64;
+    static constexpr int smem(int stages) { return 1024 + stages * (int)stage + (int)bars; }
+    static constexpr int stages = smem(kPairMaxStages) <= 232448 ? kPairMaxStages : 4;
+    static_assert(smem(stages) <= 232448 && stages >= kPairSlots, "the conversion's parity tests need stages >= slots");
+};
+
+// Wait for a phase that threads of the other block arrive on as well.
+__device__ __forceinline__ bool lin_wait_cluster(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = g_now();
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (__all_sync(0xffffffffu, done != 0u)) return true;
+        if (__any_sync(0xffffffffu, g_now() - t0 > kGemmWaitNs)) return false;
+    }
+}
+
+// Arrive on block 0's barrier at the same place as `bar`.
+__device__ __forceinline__ void lin_arrive_lead(uint32_t bar) {
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
+                 : "memory");
+}
+
+// Arrive on `bar` of both blocks once the MMAs issued so far are done.
+__device__ __forceinline__ void lin_commit_both(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
+            bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// The 4 MMAs (K = 16 each) of one column block, as g_mma_stage_ts, over both blocks.
+__device__ __forceinline__ void lin_mma_pair(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_addr, uint32_t idesc,
+                                             uint32_t accumulate) {
+    const uint64_t b0 = g_smem_desc(b_addr);
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %9, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %5, %10, p;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%2], %6, %10, 1;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%3], %7, %10, 1;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%4], %8, %10, 1;\n\t"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(a_tmem + 8u), "r"(a_tmem + 16u), "r"(a_tmem + 24u), "l"(b0), "l"(b0 + 2u), "l"(b0 + 4u),
+        "l"(b0 + 6u), "r"(accumulate), "r"(idesc)
+        : "memory");
+}
+
+template <int QB>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ LinParams P) {
+    using S = PairShape<QB>;
+    constexpr int D = S::stages;
+    extern __shared__ unsigned char g_smem[];
+    const uint32_t base = (g_smem_u32(g_smem) + 1023u) & ~1023u;
+    const uint32_t bars = base + D * S::stage;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (kPairMaxStages + s); };
+    auto wready = [&](int t) { return bars + 8u * (2 * kPairMaxStages + t); };
+    auto tfree = [&](int t) { return bars + 8u * (2 * kPairMaxStages + kPairSlots + t); };
+    const uint32_t acc_full = bars + 8u * (2 * kPairMaxStages + 2 * kPairSlots), acc_empty = acc_full + 8u;
+    const uint32_t tmem_slot = acc_full + 16u;
+    auto x_tile = [&](int s, int j) { return base + (uint32_t)s * S::stage + j * S::x_block; };
+    auto c_tile = [&](int s, int j) { return base + (uint32_t)s * S::stage + 2 * S::x_block + j * S::c_block; };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = blockIdx.x & 1u;                 // cluster dimension (2, 1, 1)
+    const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tmem_slot) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else if (threadIdx.x == 0) {
+        for (int s = 0; s < D; ++s) {
+            g_bar_init(full(s), 1);
+            g_bar_init(empty(s), 1);
+        }
+        for (int t = 0; t < kPairSlots; ++t) {
+            g_bar_init(wready(t), 8);                      // the four warps of a group in each block
+            g_bar_init(tfree(t), 1);
+        }
+        g_bar_init(acc_full, 1);
+        g_bar_init(acc_empty, 32);                         // the sixteen conversion warps of each block
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.tmap_x)) : "memory");
+    }
+    const int tts = lin_total<kPairNT>(P);                 // token tiles
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    lin_cluster_sync();                                    // the other block's barriers are ready
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
+
+    const int rtps = (P.rts + 1) >> 1, units = tts * rtps;
+    const int stages = (P.kbs + 1) >> 1;
+    bool ok = true;
+    int seq = 0;                                           // stages so far, over all units
+    if (warp == 0) {
+        int s = 0;
+        uint32_t ph = 0u;
+        for (int q = pair; q < units && ok; q += pairs) {
+            const LinUnit u = lin_find<kPairNT>(P, q / rtps);
+            // the weight rows past the last tile are converted from the last tile's codes and never stored
+            const int rt = min(2 * (q % rtps) + (int)rank, P.rts - 1);
+            const uint8_t* codes = P.tiles + ((int64_t)u.e * P.rts + rt) * P.kbs * S::c_block;
+            const int m0 = u.m0 + (int)rank * (lin_cols(u) >> 1);
+            for (int i = 0; i < stages; ++i, ++seq) {
+                if (seq >= D && !g_wait_warp(empty(s), ph ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const int kb = 2 * i, n = min(2, P.kbs - kb);
+                    g_arrive_tx(full(s), (uint32_t)n * (S::x_block + S::c_block));
+                    lin_bulk_load(c_tile(s, 0), codes + (int64_t)kb * S::c_block, (uint32_t)n * S::c_block, full(s));
+                    for (int j = 0; j < n; ++j)
+                        g_tma_load_2d(x_tile(s, j), &P.tmap_x, (kb + j) * kLinK, m0, full(s));
+                }
+                if (++s == D) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        // every copy has landed and every commit has arrived before the block may leave
+        for (int q = max(0, seq - D); q < seq; ++q)
+            if (!g_wait_warp(full(q % D), (uint32_t)((q / D) & 1)) || !g_wait_warp(empty(q % D), (uint32_t)((q / D) & 1)))
+                ok = false;
+    } else if (warp == 1) {
+        int s = 0, t = 0, done = 0;
+        uint32_t ph = 0u, tph = 0u;
+        for (int q = pair; q < units && ok; q += pairs, ++done) {
+            const LinUnit u = lin_find<kPairNT>(P, q / rtps);
+            if (rank == 0) {
+                const uint32_t idesc = gemm_idesc(2 * kLinRows, (uint32_t)lin_cols(u));
+                if (done > 0 && !lin_wait_cluster(acc_empty, (uint32_t)(done - 1) & 1u)) ok = false;
+                for (int i = 0; i < stages && ok; ++i) {
+                    if (!g_wait_warp(full(s), ph) || !lin_wait_cluster(wready(t), tph)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const int n = min(2, P.kbs - 2 * i);
+                    for (int j = 0; j < n; ++j)
+                        lin_mma_pair(tmem, tmem + kPairNT + 64u * t + 32u * j, x_tile(s, j), idesc, i | j ? 1u : 0u);
+                    lin_commit_both(empty(s));
+                    lin_commit_both(tfree(t));
+                    if (++s == D) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    if (++t == kPairSlots) {
+                        t = 0;
+                        tph ^= 1u;
+                    }
+                }
+                lin_commit_both(acc_full);
+            }
+            seq += stages;
+        }
+        for (int q = max(0, seq - kPairSlots); q < seq; ++q)
+            if (!g_wait_warp(tfree(q % kPairSlots), (uint32_t)((q / kPairSlots) & 1))) ok = false;
+    } else {
+        const int grp = (warp - 2) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        // Group grp takes the stages with seq % 4 == grp, so its TMEM slot is always the same.  (Everything that can be
+        // worked out again is: the drained sums take 64 of the 96 registers that 18 warps leave a thread.)
+        static_assert(kPairSlots == 4 && D >= 4, "the groups' slots; the ring is at least as deep");
+        const uint32_t dst = tmem + lanes + kPairNT + 64u * grp;
+        int next = grp, done = 0;                          // the group's next stage; units finished
+        int q = pair;                                      // the unit in hand
+        while (ok) {
+            const bool more = q < units && next < seq + stages;
+            // The sums of the unit before are finished when this unit's stages that fit ahead are converted: a stage
+            // beyond those needs the MMAs of its unit, and they need the drain.
+            if (seq > done * stages && (!more || next - seq >= kPairSlots)) {
+                const int rt = 2 * ((q - pairs) % rtps) + (int)rank;
+                const LinUnit u = lin_find<kPairNT>(P, (q - pairs) / rtps);
+                const int mv = u.m1 - u.m0;
+                const int64_t n = (int64_t)rt * kLinRows + r;
+                float sc = 0.0f, bi = 0.0f;
+                if (n < P.N) {
+                    sc = __half2float(__ushort_as_half(P.scale[(int64_t)u.e * P.N + n]));
+                    if (P.epi.bias) bi = lin_elem(P.epi.bias, (int64_t)u.e * P.N + n, P.epi.bias_bf16);
+                }
+                if (!g_wait_warp(acc_full, (uint32_t)done & 1u)) {
+                    ok = false;
+                    break;
+                }
+                ++done;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                float v[16][4];                            // the groups take turns of 16 tokens
+                lin_tmem_drain(tmem + lanes + 16u * grp, v);
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) lin_arrive_lead(acc_empty);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int c = 16 * grp + 64 * (j >> 2) + 4 * (j & 3);
+                    if (c < mv && n < P.N) lin_finish(P.epi, v[j], mv - c, sc, bi, (int64_t)u.m0 + c, n);
+                }
+                __syncwarp();
+                continue;
+            }
+            if (!more) {
+                if (q >= units) break;
+                seq += stages;
+                q += pairs;
+                continue;
+            }
+            // the slot first, as in linear_kernel
+            const int s = next % D;
+            if ((next >= kPairSlots && !g_wait_warp(tfree(grp), (uint32_t)(next / kPairSlots - 1) & 1u)) ||
+                !g_wait_warp(full(s), (uint32_t)(next / D) & 1u)) {
+                ok = false;
+                break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t src = c_tile(s, 0) + 16u * r;
+            lin_codes_to_tmem<QB>(src, dst);
+            if (2 * (next - seq) + 1 < P.kbs) lin_codes_to_tmem<QB>(src + S::c_block, dst + 32u);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) lin_arrive_lead(wready(grp));
+            next += kPairSlots;
+        }
+    }
+    if (!ok && lane == 0 && P.status) atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x4u);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncwarp();
+    lin_cluster_sync();                                    // nothing of this pair arrives on the other block any more
+    if (warp == 1) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
@@ -523,8 +878,10 @@ __global__ void __launch_bounds__(256) linear_empty_kernel(const __grid_constant
             e = lo;
             if (m < P.offsets[e] || m >= P.offsets[e + 1]) continue;
         }
-        for (int64_t n = threadIdx.x; n < P.N; n += blockDim.x)
-            lin_finish(P.epi, 0.0f, 0.0f, P.epi.bias ? lin_elem(P.epi.bias, e * P.N + n, P.epi.bias_bf16) : 0.0f, m, n);
+        for (int64_t n = threadIdx.x; n < P.N; n += blockDim.x) {
+            float v[1] = {0.0f};
+            lin_finish(P.epi, v, 1, 0.0f, P.epi.bias ? lin_elem(P.epi.bias, e * P.N + n, P.epi.bias_bf16) : 0.0f, m, n);
+        }
     }
 }
 
