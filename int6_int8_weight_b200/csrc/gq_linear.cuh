@@ -118,6 +118,7 @@ struct LinEpi {
     void* y;                     // [M, ldy]
     int64_t ldr, ldy;
     int32_t bias_bf16, residual_bf16, y_bf16, act;
+    int32_t rows16;              // Y and the residual are bf16 with rows of whole, aligned 16-byte pieces
 };
 
 // N values through the activation, in place.  silu and the tanh form of gelu
@@ -146,20 +147,27 @@ __device__ __forceinline__ float lin_elem(const void* p, int64_t i, int bf16) {
     return bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
-// The first `count` of N rows of Y from row m on, column n, from their sums, the
-// column's scale and bias.  The residual is read before anything is written:
-// it may be Y itself, and N loads are in flight at once.
+// The first `count` of N rows of the residual from row m on, column n, as their
+// bits (N loads in flight, which nothing waits for before the values are used).
 template <int N>
-__device__ __forceinline__ void lin_finish(const LinEpi& E, float (&v)[N], int count, float s, float b, int64_t m,
-                                           int64_t n) {
-    float r[N];
-    if (E.residual) {
-        const char* p = static_cast<const char*>(E.residual) + (m * E.ldr + n) * (E.residual_bf16 ? 2 : 4);
-        const int64_t step = E.ldr * (E.residual_bf16 ? 2 : 4);
+__device__ __forceinline__ void lin_residual(const LinEpi& E, uint32_t (&r)[N], int count, int64_t m, int64_t n) {
+    if (E.residual_bf16) {
+        const uint16_t* p = static_cast<const uint16_t*>(E.residual) + m * E.ldr + n;
 #pragma unroll
-        for (int i = 0; i < N; ++i, p += step)
-            r[i] = i >= count ? 0.0f : lin_elem(p, 0, E.residual_bf16);
+        for (int i = 0; i < N; ++i, p += E.ldr)
+            if (i < count) r[i] = *p;
+    } else {
+        const uint32_t* p = static_cast<const uint32_t*>(E.residual) + m * E.ldr + n;
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += E.ldr)
+            if (i < count) r[i] = *p;
     }
+}
+
+// N elements of a column of Y from their sums, the column's scale and bias, and
+// the residual's bits.
+template <int N>
+__device__ __forceinline__ void lin_value(const LinEpi& E, float (&v)[N], const uint32_t (&r)[N], float s, float b) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] *= s;
     if (E.bias) {
@@ -169,8 +177,16 @@ __device__ __forceinline__ void lin_finish(const LinEpi& E, float (&v)[N], int c
     lin_act(v, E.act);
     if (E.residual) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += r[i];
+        for (int i = 0; i < N; ++i) v[i] += __uint_as_float(E.residual_bf16 ? r[i] << 16 : r[i]);
     }
+}
+
+// The first `count` of them to rows m, m + 1, .. of Y, column n (the residual is
+// read by now: it may be Y itself).
+template <int N>
+__device__ __forceinline__ void lin_store(const LinEpi& E, float (&v)[N], const uint32_t (&r)[N], int count, float s,
+                                          float b, int64_t m, int64_t n) {
+    lin_value(E, v, r, s, b);
     char* p = static_cast<char*>(E.y) + (m * E.ldy + n) * (E.y_bf16 ? 2 : 4);
     const int64_t step = E.ldy * (E.y_bf16 ? 2 : 4);
 #pragma unroll
@@ -179,6 +195,14 @@ __device__ __forceinline__ void lin_finish(const LinEpi& E, float (&v)[N], int c
         if (E.y_bf16) *reinterpret_cast<uint16_t*>(p) = float_to_bf16_bits(v[i]);
         else *reinterpret_cast<float*>(p) = v[i];
     }
+}
+
+template <int N>
+__device__ __forceinline__ void lin_finish(const LinEpi& E, float (&v)[N], int count, float s, float b, int64_t m,
+                                           int64_t n) {
+    uint32_t r[N];
+    if (E.residual) lin_residual(E, r, count, m, n);
+    lin_store(E, v, r, count, s, b, m, n);
 }
 
 struct LinParams {
@@ -617,32 +641,40 @@ struct PairShape {
     static constexpr uint32_t c_block = lin_block_bytes(QB);
     static constexpr uint32_t stage = 2 * (x_block + c_block);
     static constexpr uint32_t bars = 8 * (2 * kPairMaxStages + 2 * kPairSlots + 2) + 64;
-    static constexpr int smem(int stages) { return 1024 + stages * (int)stage + (int)bars; }
+    static constexpr int smem(int stages) { return 1024 + stages * (int)stage + 16 * 256 + (int)bars; }
     static constexpr int stages = smem(kPairMaxStages) <= 232448 ? kPairMaxStages : 4;
     static_assert(smem(stages) <= 232448 && stages >= kPairSlots, "the conversion's parity tests need stages >= slots");
 };
 
-// Wait for a phase that threads of the other block arrive on as well.
-__device__ __forceinline__ bool lin_wait_cluster(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = g_now();
-    for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n .reg .pred p;\n"
-            " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-            " selp.u32 %0, 1, 0, p;\n}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(20000u)
-            : "memory");
-        if (__all_sync(0xffffffffu, done != 0u)) return true;
-        if (__any_sync(0xffffffffu, g_now() - t0 > kGemmWaitNs)) return false;
-    }
+__device__ __forceinline__ void lin_sts128(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lin_lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void lin_sts16(uint32_t addr, uint16_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t lin_lds16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
 }
 
-// Arrive on block 0's barrier at the same place as `bar`.
+// Arrive on block 0's barrier at the same place as `bar`.  What it announces is
+// in tensor memory (ordered by the tcgen05 fences) or came by a copy that the
+// arriving thread has waited for, so the default scope will do; a release at
+// cluster scope waits for the thread's earlier stores to reach the other SM
+// (M 4096, N = K = 8192: 381 us against 355).
 __device__ __forceinline__ void lin_arrive_lead(uint32_t bar) {
     asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-                 "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
+                 "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
                  : "memory");
 }
 
@@ -681,7 +713,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     constexpr int D = S::stages;
     extern __shared__ unsigned char g_smem[];
     const uint32_t base = (g_smem_u32(g_smem) + 1023u) & ~1023u;
-    const uint32_t bars = base + D * S::stage;
+    const uint32_t stg = base + D * S::stage, bars = stg + 16 * 256;   // 256 bytes a conversion warp, barriers
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (kPairMaxStages + s); };
     auto wready = [&](int t) { return bars + 8u * (2 * kPairMaxStages + t); };
@@ -732,6 +764,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int rt = min(2 * (q % rtps) + (int)rank, P.rts - 1);
             const uint8_t* codes = P.tiles + ((int64_t)u.e * P.rts + rt) * P.kbs * S::c_block;
             const int m0 = u.m0 + (int)rank * (lin_cols(u) >> 1);
+            if (P.epi.residual) {                          // the unit's share of the residual into L2
+                const int es = P.epi.residual_bf16 ? 2 : 4;
+                const int64_t n0 = (int64_t)(2 * (q % rtps) + (int)rank) * kLinRows, n1 = min(n0 + kLinRows, P.N);
+                for (int m = u.m0 + lane; m < u.m1; m += 32)
+                    for (int64_t n = n0; n < n1; n += 128 / es)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(P.epi.residual) +
+                                                                      (m * P.epi.ldr + n) * es));
+                __syncwarp();
+            }
             for (int i = 0; i < stages; ++i, ++seq) {
                 if (seq >= D && !g_wait_warp(empty(s), ph ^ 1u)) {
                     ok = false;
@@ -761,9 +802,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const LinUnit u = lin_find<kPairNT>(P, q / rtps);
             if (rank == 0) {
                 const uint32_t idesc = gemm_idesc(2 * kLinRows, (uint32_t)lin_cols(u));
-                if (done > 0 && !lin_wait_cluster(acc_empty, (uint32_t)(done - 1) & 1u)) ok = false;
+                if (done > 0 && !g_wait_warp(acc_empty, (uint32_t)(done - 1) & 1u)) ok = false;
                 for (int i = 0; i < stages && ok; ++i) {
-                    if (!g_wait_warp(full(s), ph) || !lin_wait_cluster(wready(t), tph)) {
+                    if (!g_wait_warp(full(s), ph) || !g_wait_warp(wready(t), tph)) {
                         ok = false;
                         break;
                     }
@@ -811,6 +852,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     sc = __half2float(__ushort_as_half(P.scale[(int64_t)u.e * P.N + n]));
                     if (P.epi.bias) bi = lin_elem(P.epi.bias, (int64_t)u.e * P.N + n, P.epi.bias_bf16);
                 }
+                // In the 16-byte form of the epilogue below: this lane's piece of a row, and the residual's first 16 tokens,
+                // on their way while the MMAs end (from L2: the copying warp asked for them when the unit began).
+                const int64_t n8 = n - lane + 8 * (lane & 3);
+                const bool in8 = n8 < P.N, add = P.epi.residual && P.epi.rows16;   // (N is a multiple of 8 then)
+                const uint32_t buf = stg + 256u * (uint32_t)(warp - 2);
+                auto fetch = [&](int c8) {                 // pieces of eight tokens
+                    const int m = c8 + (lane >> 2);
+                    return add && in8 && m < mv ? __ldcg(reinterpret_cast<const uint4*>(
+                                                      static_cast<const uint16_t*>(P.epi.residual) +
+                                                      ((int64_t)u.m0 + m) * P.epi.ldr + n8))
+                                                : make_uint4(0u, 0u, 0u, 0u);
+                };
+                uint4 ahead[2] = {fetch(16 * grp), fetch(16 * grp + 8)};
                 if (!g_wait_warp(acc_full, (uint32_t)done & 1u)) {
                     ok = false;
                     break;
@@ -822,10 +876,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) lin_arrive_lead(acc_empty);
+                // Runs of 16 tokens, in a rolled loop that moves the sums down by one run: unrolled, the code was fetched
+                // more slowly than it ran.
+                if (P.epi.rows16) {
+                    // bf16, rows of 16-byte pieces: four tokens of the warp's 32 columns (256 bytes) change hands in shared
+                    // memory, so that the residual comes and Y leaves in pieces of 16 bytes.
+                    int c = 16 * grp;
+#pragma unroll 1
+                    for (int run = 0; run < 4 && c < mv; ++run, c += 64) {
+                        uint16_t* y = static_cast<uint16_t*>(P.epi.y) + ((int64_t)u.m0 + c + (lane >> 2)) * P.epi.ldy + n8;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int c = 16 * grp + 64 * (j >> 2) + 4 * (j & 3);
-                    if (c < mv && n < P.N) lin_finish(P.epi, v[j], mv - c, sc, bi, (int64_t)u.m0 + c, n);
+                        for (int j = 0; j < 4; ++j, y += 4 * P.epi.ldy) {
+                            uint32_t rs[4] = {0u, 0u, 0u, 0u};
+                            if (add) {
+                                if ((lane >> 4) == (j & 1)) lin_sts128(buf + 16u * (lane & 15), ahead[j >> 1]);
+                                __syncwarp();
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) rs[i] = lin_lds16(buf + 64u * i + 2u * lane);
+                                __syncwarp();
+                                if (j & 1) ahead[j >> 1] = run < 3 ? fetch(c + 64 + 4 * (j - 1)) : ahead[j >> 1];
+                            }
+                            lin_value(P.epi, v[j], rs, sc, bi);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) lin_sts16(buf + 64u * i + 2u * lane, float_to_bf16_bits(v[j][i]));
+                            __syncwarp();
+                            if (lane < 16 && in8 && c + 4 * j + (lane >> 2) < mv)
+                                *reinterpret_cast<uint4*>(y) = lin_lds128(buf + 16u * lane);
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int j = 0; j < 12; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[j][i] = v[j + 4][i];
+                    }
+                } else {
+                    const bool in = n < P.N;
+                    int c = 16 * grp;
+#pragma unroll 1
+                    for (int run = 0; run < 4; ++run, c += 48) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j, c += 4)
+                            if (in && c < mv) lin_finish(P.epi, v[j], mv - c, sc, bi, (int64_t)u.m0 + c, n);
+#pragma unroll
+                        for (int j = 0; j < 12; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[j][i] = v[j + 4][i];
+                    }
                 }
                 __syncwarp();
                 continue;
