@@ -140,9 +140,7 @@ gq_status linear(const void* d_x, int64_t M, int64_t K, int64_t ldx, const int32
     P.kbs = (int32_t)((K + kLinK - 1) / kLinK);
     P.rts = (int32_t)((N + kLinRows - 1) / kLinRows);
     P.epi = LinEpi{e.bias, e.residual, d_y, e.ldr, ldy, e.bias_dtype == GQ_BF16, e.residual_dtype == GQ_BF16,
-                   e.y_dtype == GQ_BF16, e.act, 0};
-    P.epi.rows16 = P.epi.y_bf16 && N % 8 == 0 && aligned(d_y, 16) && ldy % 8 == 0 &&
-                   (!e.residual || (P.epi.residual_bf16 && aligned(e.residual, 16) && e.ldr % 8 == 0));
+                   e.y_dtype == GQ_BF16, e.act};
     if (K == 0) {
         linear_empty_kernel<<<(unsigned)std::min<int64_t>(M, 65535), 256, 0, stream>>>(P);
         return launch_status();

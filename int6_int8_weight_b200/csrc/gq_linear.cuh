@@ -118,7 +118,6 @@ struct LinEpi {
     void* y;                     // [M, ldy]
     int64_t ldr, ldy;
     int32_t bias_bf16, residual_bf16, y_bf16, act;
-    int32_t rows16;              // Y and the residual are bf16 with rows of whole, aligned 16-byte pieces
 };
 
 // N values through the activation, in place.  silu and the tanh form of gelu
@@ -631,7 +630,8 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
 // Block 0's barriers gather both blocks' conversions (wready) and drains
 // (acc_empty); the MMAs' commits arrive on both blocks' barriers.
 constexpr int kPairNT = 256;
-constexpr int kPairThreads = 64 + 512;
+constexpr int kPairThreads = 128 + 512;
+constexpr int kPairRoleRegs = 32, kPairConvRegs = 112;     // 4 * 32 + 16 * 112 = 20 * 96: what the block is launched with
 constexpr int kPairSlots = 4;
 constexpr int kPairMaxStages = 5;
 
@@ -641,31 +641,10 @@ struct PairShape {
     static constexpr uint32_t c_block = lin_block_bytes(QB);
     static constexpr uint32_t stage = 2 * (x_block + c_block);
     static constexpr uint32_t bars = 8 * (2 * kPairMaxStages + 2 * kPairSlots + 2) + 64;
-    static constexpr int smem(int stages) { return 1024 + stages * (int)stage + 16 * 256 + (int)bars; }
+    static constexpr int smem(int stages) { return 1024 + stages * (int)stage + (int)bars; }
     static constexpr int stages = smem(kPairMaxStages) <= 232448 ? kPairMaxStages : 4;
     static_assert(smem(stages) <= 232448 && stages >= kPairSlots, "the conversion's parity tests need stages >= slots");
 };
-
-__device__ __forceinline__ void lin_sts128(uint32_t addr, const uint4& v) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 lin_lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ void lin_sts16(uint32_t addr, uint16_t v) {
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t lin_lds16(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-    return v;
-}
 
 // Arrive on block 0's barrier at the same place as `bar`.  What it announces is
 // in tensor memory (ordered by the tcgen05 fences) or came by a copy that the
@@ -713,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     constexpr int D = S::stages;
     extern __shared__ unsigned char g_smem[];
     const uint32_t base = (g_smem_u32(g_smem) + 1023u) & ~1023u;
-    const uint32_t stg = base + D * S::stage, bars = stg + 16 * 256;   // 256 bytes a conversion warp, barriers
+    const uint32_t bars = base + D * S::stage;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (kPairMaxStages + s); };
     auto wready = [&](int t) { return bars + 8u * (2 * kPairMaxStages + t); };
@@ -755,6 +734,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int stages = (P.kbs + 1) >> 1;
     bool ok = true;
     int seq = 0;                                           // stages so far, over all units
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRoleRegs));
     if (warp == 0) {
         int s = 0;
         uint32_t ph = 0u;
@@ -829,105 +809,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         for (int q = max(0, seq - kPairSlots); q < seq; ++q)
             if (!g_wait_warp(tfree(q % kPairSlots), (uint32_t)((q / kPairSlots) & 1))) ok = false;
-    } else {
-        const int grp = (warp - 2) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
+    } else if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairConvRegs));
+        const int grp = (warp - 4) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         // Group grp takes the stages with seq % 4 == grp, so its TMEM slot is always the same.  (Everything that can be
         // worked out again is: the drained sums take 64 of the 96 registers that 18 warps leave a thread.)
         static_assert(kPairSlots == 4 && D >= 4, "the groups' slots; the ring is at least as deep");
         const uint32_t dst = tmem + lanes + kPairNT + 64u * grp;
-        int next = grp, done = 0;                          // the group's next stage; units finished
+        int next = grp, done = 0;                          // the group's next stage; units whose sums are drained
         int q = pair;                                      // the unit in hand
+        float v[16][4];                                    // drained sums: runs of 16 tokens, 64 tokens apart
+        int left = 0, c = 0;                               // runs still to be finished, and the first token of the next
+        int m0 = 0, mv = 0, n = 0;                         // of the unit that they belong to: its rows of X, this thread's
+                                                           // column, the column's scale and bias
+        float sc = 0.0f, bi = 0.0f;
+        bool turn = false;                                 // whether a run is next, or a stage
         while (ok) {
-            const bool more = q < units && next < seq + stages;
-            // The sums of the unit before are finished when this unit's stages that fit ahead are converted: a stage
-            // beyond those needs the MMAs of its unit, and they need the drain.
-            if (seq > done * stages && (!more || next - seq >= kPairSlots)) {
-                const int rt = 2 * ((q - pairs) % rtps) + (int)rank;
-                const LinUnit u = lin_find<kPairNT>(P, (q - pairs) / rtps);
-                const int mv = u.m1 - u.m0;
-                const int64_t n = (int64_t)rt * kLinRows + r;
-                float sc = 0.0f, bi = 0.0f;
+            const bool more = q < units && next < seq + stages, pending = seq > done * stages;
+            if (left > 0 && (turn || !more)) {
+                // Four tokens at a time, the residual of the next four on its way (from L2: the copying warp asked for
+                // it when the unit began).
+                turn = false;
+                --left;
                 if (n < P.N) {
-                    sc = __half2float(__ushort_as_half(P.scale[(int64_t)u.e * P.N + n]));
-                    if (P.epi.bias) bi = lin_elem(P.epi.bias, (int64_t)u.e * P.N + n, P.epi.bias_bf16);
+                    uint32_t rs[2][4];
+                    if (P.epi.residual && c < mv) lin_residual(P.epi, rs[0], mv - c, (int64_t)m0 + c, n);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c0 = c + 4 * j;
+                        if (P.epi.residual && j < 3 && c0 + 4 < mv)
+                            lin_residual(P.epi, rs[(j + 1) & 1], mv - c0 - 4, (int64_t)m0 + c0 + 4, n);
+                        if (c0 < mv) lin_store(P.epi, v[j], rs[j & 1], mv - c0, sc, bi, (int64_t)m0 + c0, n);
+                    }
                 }
-                // In the 16-byte form of the epilogue below: this lane's piece of a row, and the residual's first 16 tokens,
-                // on their way while the MMAs end (from L2: the copying warp asked for them when the unit began).
-                const int64_t n8 = n - lane + 8 * (lane & 3);
-                const bool in8 = n8 < P.N, add = P.epi.residual && P.epi.rows16;   // (N is a multiple of 8 then)
-                const uint32_t buf = stg + 256u * (uint32_t)(warp - 2);
-                auto fetch = [&](int c8) {                 // pieces of eight tokens
-                    const int m = c8 + (lane >> 2);
-                    return add && in8 && m < mv ? __ldcg(reinterpret_cast<const uint4*>(
-                                                      static_cast<const uint16_t*>(P.epi.residual) +
-                                                      ((int64_t)u.m0 + m) * P.epi.ldr + n8))
-                                                : make_uint4(0u, 0u, 0u, 0u);
-                };
-                uint4 ahead[2] = {fetch(16 * grp), fetch(16 * grp + 8)};
+                c += 64;
+#pragma unroll
+                for (int j = 0; j < 12; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[j][i] = v[j + 4][i];
+                __syncwarp();
+                continue;
+            }
+            // The sums of the unit before are drained when the MMAs have done their last stage, which is also when the last
+            // of the four slots comes free: the group that waits for that slot drains first.
+            if (pending && (!more || next - seq >= kPairSlots - 1)) {
                 if (!g_wait_warp(acc_full, (uint32_t)done & 1u)) {
                     ok = false;
                     break;
                 }
                 ++done;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                float v[16][4];                            // the groups take turns of 16 tokens
                 lin_tmem_drain(tmem + lanes + 16u * grp, v);
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) lin_arrive_lead(acc_empty);
-                // Runs of 16 tokens, in a rolled loop that moves the sums down by one run: unrolled, the code was fetched
-                // more slowly than it ran.
-                if (P.epi.rows16) {
-                    // bf16, rows of 16-byte pieces: four tokens of the warp's 32 columns (256 bytes) change hands in shared
-                    // memory, so that the residual comes and Y leaves in pieces of 16 bytes.
-                    int c = 16 * grp;
-#pragma unroll 1
-                    for (int run = 0; run < 4 && c < mv; ++run, c += 64) {
-                        uint16_t* y = static_cast<uint16_t*>(P.epi.y) + ((int64_t)u.m0 + c + (lane >> 2)) * P.epi.ldy + n8;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j, y += 4 * P.epi.ldy) {
-                            uint32_t rs[4] = {0u, 0u, 0u, 0u};
-                            if (add) {
-                                if ((lane >> 4) == (j & 1)) lin_sts128(buf + 16u * (lane & 15), ahead[j >> 1]);
-                                __syncwarp();
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) rs[i] = lin_lds16(buf + 64u * i + 2u * lane);
-                                __syncwarp();
-                                if (j & 1) ahead[j >> 1] = run < 3 ? fetch(c + 64 + 4 * (j - 1)) : ahead[j >> 1];
-                            }
-                            lin_value(P.epi, v[j], rs, sc, bi);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) lin_sts16(buf + 64u * i + 2u * lane, float_to_bf16_bits(v[j][i]));
-                            __syncwarp();
-                            if (lane < 16 && in8 && c + 4 * j + (lane >> 2) < mv)
-                                *reinterpret_cast<uint4*>(y) = lin_lds128(buf + 16u * lane);
-                            __syncwarp();
-                        }
-#pragma unroll
-                        for (int j = 0; j < 12; ++j)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[j][i] = v[j + 4][i];
-                    }
-                } else {
-                    const bool in = n < P.N;
-                    int c = 16 * grp;
-#pragma unroll 1
-                    for (int run = 0; run < 4; ++run, c += 48) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j, c += 4)
-                            if (in && c < mv) lin_finish(P.epi, v[j], mv - c, sc, bi, (int64_t)u.m0 + c, n);
-#pragma unroll
-                        for (int j = 0; j < 12; ++j)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[j][i] = v[j + 4][i];
-                    }
-                }
-                __syncwarp();
+                c = 16 * grp;
+                left = (mv - c + 63) >> 6;                 // (not positive where the unit has no token for the group)
+                turn = next - seq >= kPairSlots;
                 continue;
             }
             if (!more) {
                 if (q >= units) break;
+                const LinUnit u = lin_find<kPairNT>(P, q / rtps);
+                m0 = u.m0;
+                mv = u.m1 - u.m0;
+                n = (2 * (q % rtps) + (int)rank) * kLinRows + r;
+                if (n < P.N) {
+                    sc = __half2float(__ushort_as_half(P.scale[(int64_t)u.e * P.N + n]));
+                    bi = P.epi.bias ? lin_elem(P.epi.bias, (int64_t)u.e * P.N + n, P.epi.bias_bf16) : 0.0f;
+                }
                 seq += stages;
                 q += pairs;
                 continue;
@@ -948,6 +899,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             __syncwarp();
             if (lane == 0) lin_arrive_lead(wready(grp));
             next += kPairSlots;
+            turn = true;
         }
     }
     if (!ok && lane == 0 && P.status) atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x4u);
