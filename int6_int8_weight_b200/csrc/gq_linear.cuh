@@ -126,19 +126,24 @@ struct LinEpi {
 // stays NaN.
 template <int N>
 __device__ __forceinline__ void lin_act(float (&z)[N], int act) {
-    if (act == GQ_ACT_NONE) return;
+    // one test of `act` for all of them, and a loop of its own for each
+    auto each = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float x = z[i];
-        if (act <= GQ_ACT_LEAKY_RELU2) {
-            const float r = x < 0.0f ? (act == GQ_ACT_LEAKY_RELU2 ? 0.5f * x : 0.0f) : x;
-            z[i] = act == GQ_ACT_RELU ? r : r * r;
-        } else if (act == GQ_ACT_GELU) {
-            z[i] = 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
-        } else {
-            const float w = act == GQ_ACT_SILU ? x : 1.5957691216057308f * __fmaf_rn(0.044715f * x, x * x, x);
-            z[i] = __fdividef(x, 1.0f + __expf(-w));
-        }
+        for (int i = 0; i < N; ++i) z[i] = f(z[i]);
+    };
+    switch (act) {
+        case GQ_ACT_RELU: each([](float x) { return x < 0.0f ? 0.0f : x; }); break;
+        case GQ_ACT_RELU2: each([](float x) { x = x < 0.0f ? 0.0f : x; return x * x; }); break;
+        case GQ_ACT_LEAKY_RELU2: each([](float x) { x = x < 0.0f ? 0.5f * x : x; return x * x; }); break;
+        case GQ_ACT_SILU: each([](float x) { return __fdividef(x, 1.0f + __expf(-x)); }); break;
+        case GQ_ACT_GELU: each([](float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f)); }); break;
+        case GQ_ACT_GELU_TANH:
+            each([](float x) {
+                const float w = 1.5957691216057308f * __fmaf_rn(0.044715f * x, x * x, x);
+                return __fdividef(x, 1.0f + __expf(-w));
+            });
+            break;
+        default: break;
     }
 }
 
@@ -146,27 +151,26 @@ __device__ __forceinline__ float lin_elem(const void* p, int64_t i, int bf16) {
     return bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
-// The first `count` of N rows of the residual from row m on, column n, as their
-// bits (N loads in flight, which nothing waits for before the values are used).
-template <int N>
-__device__ __forceinline__ void lin_residual(const LinEpi& E, uint32_t (&r)[N], int count, int64_t m, int64_t n) {
-    if (E.residual_bf16) {
-        const uint16_t* p = static_cast<const uint16_t*>(E.residual) + m * E.ldr + n;
+// N rows of Y from row m on, column n (the first `count` of them), from their
+// sums, the column's scale and bias.  The residual is read before anything is
+// written (it may be Y itself), all N loads in flight while the activation is
+// worked out.  Whole runs are told apart from the last rows of a tile: a test
+// and a branch for each element cost as much as the rest.
+template <bool WHOLE, int N>
+__device__ __forceinline__ void lin_rows_out(const LinEpi& E, float (&v)[N], int count, float s, float b, int64_t m,
+                                             int64_t n) {
+    uint32_t r[N];
+    if (E.residual) {
+        if (E.residual_bf16) {
+            const uint16_t* p = static_cast<const uint16_t*>(E.residual) + m * E.ldr + n;
 #pragma unroll
-        for (int i = 0; i < N; ++i, p += E.ldr)
-            if (i < count) r[i] = *p;
-    } else {
-        const uint32_t* p = static_cast<const uint32_t*>(E.residual) + m * E.ldr + n;
+            for (int i = 0; i < N; ++i, p += E.ldr) r[i] = WHOLE || i < count ? (uint32_t)*p : 0u;
+        } else {
+            const uint32_t* p = static_cast<const uint32_t*>(E.residual) + m * E.ldr + n;
 #pragma unroll
-        for (int i = 0; i < N; ++i, p += E.ldr)
-            if (i < count) r[i] = *p;
+            for (int i = 0; i < N; ++i, p += E.ldr) r[i] = WHOLE || i < count ? *p : 0u;
+        }
     }
-}
-
-// N elements of a column of Y from their sums, the column's scale and bias, and
-// the residual's bits.
-template <int N>
-__device__ __forceinline__ void lin_value(const LinEpi& E, float (&v)[N], const uint32_t (&r)[N], float s, float b) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] *= s;
     if (E.bias) {
@@ -175,33 +179,28 @@ __device__ __forceinline__ void lin_value(const LinEpi& E, float (&v)[N], const 
     }
     lin_act(v, E.act);
     if (E.residual) {
+        const int shift = E.residual_bf16 ? 16 : 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __uint_as_float(E.residual_bf16 ? r[i] << 16 : r[i]);
+        for (int i = 0; i < N; ++i) v[i] += __uint_as_float(r[i] << shift);
     }
-}
-
-// The first `count` of them to rows m, m + 1, .. of Y, column n (the residual is
-// read by now: it may be Y itself).
-template <int N>
-__device__ __forceinline__ void lin_store(const LinEpi& E, float (&v)[N], const uint32_t (&r)[N], int count, float s,
-                                          float b, int64_t m, int64_t n) {
-    lin_value(E, v, r, s, b);
-    char* p = static_cast<char*>(E.y) + (m * E.ldy + n) * (E.y_bf16 ? 2 : 4);
-    const int64_t step = E.ldy * (E.y_bf16 ? 2 : 4);
+    if (E.y_bf16) {
+        uint16_t* p = static_cast<uint16_t*>(E.y) + m * E.ldy + n;
 #pragma unroll
-    for (int i = 0; i < N; ++i, p += step) {
-        if (i >= count) break;
-        if (E.y_bf16) *reinterpret_cast<uint16_t*>(p) = float_to_bf16_bits(v[i]);
-        else *reinterpret_cast<float*>(p) = v[i];
+        for (int i = 0; i < N; ++i, p += E.ldy)
+            if (WHOLE || i < count) *p = float_to_bf16_bits(v[i]);
+    } else {
+        float* p = static_cast<float*>(E.y) + m * E.ldy + n;
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += E.ldy)
+            if (WHOLE || i < count) *p = v[i];
     }
 }
 
 template <int N>
 __device__ __forceinline__ void lin_finish(const LinEpi& E, float (&v)[N], int count, float s, float b, int64_t m,
                                            int64_t n) {
-    uint32_t r[N];
-    if (E.residual) lin_residual(E, r, count, m, n);
-    lin_store(E, v, r, count, s, b, m, n);
+    if (count >= N) lin_rows_out<true>(E, v, count, s, b, m, n);
+    else lin_rows_out<false>(E, v, count, s, b, m, n);
 }
 
 struct LinParams {
@@ -828,20 +827,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         while (ok) {
             const bool more = q < units && next < seq + stages, pending = seq > done * stages;
             if (left > 0 && (turn || !more)) {
-                // Four tokens at a time, the residual of the next four on its way (from L2: the copying warp asked for
-                // it when the unit began).
                 turn = false;
                 --left;
-                if (n < P.N) {
-                    uint32_t rs[2][4];
-                    if (P.epi.residual && c < mv) lin_residual(P.epi, rs[0], mv - c, (int64_t)m0 + c, n);
+                if (n < P.N && c < mv) {                   // (the residual is in L2: the copying warp asked for it)
+                    float z[16];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int c0 = c + 4 * j;
-                        if (P.epi.residual && j < 3 && c0 + 4 < mv)
-                            lin_residual(P.epi, rs[(j + 1) & 1], mv - c0 - 4, (int64_t)m0 + c0 + 4, n);
-                        if (c0 < mv) lin_store(P.epi, v[j], rs[j & 1], mv - c0, sc, bi, (int64_t)m0 + c0, n);
-                    }
+                    for (int i = 0; i < 16; ++i) z[i] = v[i >> 2][i & 3];
+                    lin_finish(P.epi, z, mv - c, sc, bi, (int64_t)m0 + c, n);
                 }
                 c += 64;
 #pragma unroll
