@@ -2,7 +2,6 @@
 // gq_gemm_grouped (include/gq.h): argument checks, launch planning, launches.
 #include <algorithm>
 #include <atomic>
-#include <cstdlib>
 #include <cstring>
 
 #include "gq_host.h"
@@ -39,8 +38,14 @@ gq_status launch(LinParams& P, const void* d_x, int64_t K, int64_t ldx, cudaStre
     const int64_t tts = P.offsets ? P.M / NT + std::min<int64_t>(P.E, P.M) : (P.M + NT - 1) / NT;
     const int64_t units = tts * P.rts;
     if (units > INT32_MAX) return GQ_ERR_UNSUPPORTED;
+    // The split: blocks for every SM once, as far as a cluster of 4 (of 8 where a tile or few are all there is: clusters
+    // of 8 find room on fewer SMs); then twice, if each block keeps 12 column blocks to stream.  N = K = 2048, M 16:
+    // 11.1, 8.5, 7.0, 7.8 us with 1, 2, 4, 8 blocks a tile; N = K = 8192: 32.7, 20.7, 18.1, 23.9; N 1792, K 512, M 333:
+    // 9.2, 8.8, 10.4, 19.4.
+    const int64_t sms = sm_count();
     int ls = 0;
-    while (ls < 3 && (units << (ls + 1)) <= 2 * (int64_t)sm_count() && P.kbs >= 4 << ls) ++ls;
+    while (ls < (units <= 8 ? 3 : 2) && (units << (ls + 1)) <= sms && P.kbs >= 2 << (ls + 1)) ++ls;
+    if (ls < 2 && (units << (ls + 1)) <= 2 * sms && P.kbs >= 12 << (ls + 1)) ++ls;
     if (units << ls > INT32_MAX) return GQ_ERR_UNSUPPORTED;
     P.log_split = ls;
     const int split = 1 << ls;
@@ -69,11 +74,16 @@ gq_status launch(LinParams& P, const void* d_x, int64_t K, int64_t ldx, cudaStre
     return cuda_status(cudaLaunchKernelEx(&cfg, linear_kernel<QB, NT>, static_cast<const LinParams&>(P)));
 }
 
-// Whether the pair kernel is the faster one.
+// Whether the pair kernel is the faster one: 24 column blocks at least, so that a unit's hand-over counts for little;
+// enough rows that a converted code serves more tokens than the 128 of the other kernel's tiles, or nearly; and
+// units that fill the pairs' rounds to three fifths.  Measured, us, one block a tile against pairs: N = K = 8192: M 384
+// 68.1 / 48.3, M 256 41.9 / 50.8; N 8192, K 2048: M 384 23.7 / 21.2, M 2048 80.8 / 70.3; N 1536, K 512: M 1024 17.2 /
+// 15.8, M 2048 12.3 / 16.1; 32 experts of 4096 x 2048: 160 rows each 142 / 127, 512 rows 330 / 283.
 bool pair_pays(const LinParams& P) {
-    const char* f = getenv("LIN_PAIR");
-    if (f) return f[0] == '1';
-    return P.M / P.E >= 192;
+    const int64_t rows = (P.M + P.E - 1) / P.E, pairs = std::max(1, sm_count() / 2);
+    const int64_t units = (P.rts + 1) / 2 * (int64_t)P.E * ((rows + kPairNT - 1) / kPairNT);
+    const int64_t rounds = (units + pairs - 1) / pairs;
+    return P.kbs >= 24 && rows >= 96 && 5 * units >= 3 * rounds * pairs;
 }
 
 // The kernel of 256 x 256 tiles over pairs of SMs.

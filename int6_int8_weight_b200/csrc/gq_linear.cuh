@@ -264,6 +264,24 @@ __device__ __forceinline__ float lin_ld_peer(uint32_t addr, uint32_t rank) {
     return f;
 }
 
+// Four consecutive rows of a column from the S blocks' sums at shared address
+// `at`, added in rank order: all 4 S loads are on their way before the first
+// addition.
+template <int S>
+__device__ __forceinline__ void lin_gather(float (&v)[4], uint32_t at) {
+    float t[S][4];
+#pragma unroll
+    for (int q = 0; q < S; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[q][i] = lin_ld_peer(at + 512u * i, (uint32_t)q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = t[0][i];
+#pragma unroll
+        for (int q = 1; q < S; ++q) v[i] += t[q][i];
+    }
+}
+
 __device__ __forceinline__ void lin_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -592,15 +610,17 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
     __syncwarp();
     if (split > 1 && mv > 0) {                           // the same in every block of the cluster
         lin_cluster_sync();
-        // rows of Y by 128 threads each over the cluster; a thread keeps its column
+        // four rows of Y by 128 threads at a time over the cluster; a thread keeps its column
         constexpr int kLines = S::threads / kLinRows;
         const int line = (int)threadIdx.x / kLinRows;
         if (line < kLines && n < P.N)
-            for (int c = (int)rank * kLines + line; c < mv; c += (int)split * kLines) {
+            for (int c = 4 * ((int)rank * kLines + line); c < mv; c += 4 * (int)split * kLines) {
                 const uint32_t at = base + 4u * (uint32_t)(c * kLinRows + ((int)threadIdx.x & 127));
-                float v[1] = {0.0f};
-                for (int q = 0; q < (int)split; ++q) v[0] += lin_ld_peer(at, (uint32_t)q);
-                lin_finish(P.epi, v, 1, sc, bi, (int64_t)u.m0 + c, n);
+                float v[4];                                // (rows past mv: whatever the sums' memory holds, not stored)
+                if (split == 2) lin_gather<2>(v, at);
+                else if (split == 4) lin_gather<4>(v, at);
+                else lin_gather<8>(v, at);
+                lin_finish(P.epi, v, mv - c, sc, bi, (int64_t)u.m0 + c, n);
             }
         lin_cluster_sync();                                // its memory is read until here
     }
