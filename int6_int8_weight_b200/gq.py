@@ -592,32 +592,40 @@ def _rows(t, M, N):
 def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, out_dtype, stream, check_status):
     """Argument checks and the call shared by gemm_epilogue and gemm_grouped.
     (Written for few Python operations: a small layer's kernel takes less time than they do.)"""
-    if x.dtype is not torch.bfloat16 or x.dim() != 2 or (ldx := _rows(x, *x.shape)) is None:
+    if x.dtype is not torch.bfloat16 or x.dim() != 2:
         raise ValueError("x must be a bf16 [M, K] tensor with contiguous rows")
     M, K = x.shape
+    ldx, one = x.stride()
     if M <= 1 or K == 0:
         ldx = -(-K // 8) * 8                               # no second row: any pitch will do
+    if (one != 1 and K > 1 and M > 0) or ldx < K:
+        raise ValueError("x must be a bf16 [M, K] tensor with contiguous rows")
     shape = scale.shape
     if scale.dtype is not torch.float16 or len(shape) != (1 if offsets is None else 2) or not scale.is_contiguous():
         raise ValueError("scale_f16 must be a contiguous fp16 tensor, [N] (grouped: [E, N])")
     N = shape[-1]
     nbytes = ((N + 127) >> 7) * ((K + 63) >> 6) * (6144 if qbits == 6 else 8192)
-    if qbits not in (6, 8) or tiles.dtype is not torch.uint8 or tiles.shape != (*shape[:-1], nbytes) \
+    if (qbits != 6 and qbits != 8) or tiles.dtype is not torch.uint8 or tiles.shape != (*shape[:-1], nbytes) \
             or not tiles.is_contiguous():
         raise ValueError("tiles must be what tile_weight gives for these N, K and qbits")
     code = ACTS.get(act)
     if code is None:
         raise ValueError(f"act is one of {', '.join(ACTS)}")
-    if y is None:
-        y = x.new_empty((M, N), dtype=out_dtype or torch.bfloat16)
-        ldy = N
-    elif (ldy := _rows(y, M, N)) is None or (out_dtype is not None and y.dtype is not out_dtype):
-        raise ValueError("y must be [M, N] with contiguous rows and of out_dtype where that is given")
-    y_code = _DTYPE_CODES.get(y.dtype)
-    if y_code is None:
-        raise TypeError(f"Y is float32 or bfloat16, got {y.dtype}")
     dev = x.get_device()
-    same = tiles.get_device() == dev == scale.get_device() == y.get_device()
+    same = tiles.get_device() == dev == scale.get_device()
+    if y is None:
+        y_code = 1 if out_dtype is None else _DTYPE_CODES.get(out_dtype)
+        if y_code is not None and same and dev >= 0:
+            y = x.new_empty((M, N), dtype=out_dtype or torch.bfloat16)
+        ldy = N
+    else:
+        ldy = _rows(y, M, N)
+        if ldy is None or (out_dtype is not None and y.dtype is not out_dtype):
+            raise ValueError("y must be [M, N] with contiguous rows and of out_dtype where that is given")
+        y_code = _DTYPE_CODES.get(y.dtype)
+        same = same and y.get_device() == dev
+    if y_code is None:
+        raise TypeError("Y is float32 or bfloat16")
     if bias is None and residual is None:
         epi = _EPILOGUE_NONE[code, y_code]
     else:
@@ -634,12 +642,17 @@ def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, o
             r, r_code = residual.data_ptr(), _dtype_code(residual)
             same = same and residual.get_device() == dev
         epi = _EPILOGUE.pack(b, r, ldr, b_code, r_code, code, y_code)
-    if not same or (offsets is not None and offsets.get_device() != dev):
-        raise ValueError("every tensor of a call lies on one device")
+    if dev < 0 or not same or (offsets is not None and offsets.get_device() != dev):
+        raise ValueError("every tensor of a call lies on one CUDA device")
     st = torch.empty(1, dtype=torch.int32, device=x.device) if check_status else None
-    group = () if offsets is None else (offsets.data_ptr(), shape[0])
-    status = _on(dev, stream, fn, x.data_ptr(), M, K, ldx, *group, tiles.data_ptr(), scale.data_ptr(), qbits, N, epi,
-                 y.data_ptr(), ldy, None if st is None else st.data_ptr())
+    args = (x.data_ptr(), M, K, ldx, tiles.data_ptr(), scale.data_ptr(), qbits, N, epi, y.data_ptr(), ldy,
+            None if st is None else st.data_ptr())
+    if offsets is not None:
+        args = (*args[:4], offsets.data_ptr(), shape[0], *args[4:])
+    if stream is None and dev == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        status = _on(dev, stream, fn, *args)
     if status:
         _check(status, where)
     if check_status and (v := int(st.item())):
