@@ -321,6 +321,15 @@ __device__ __forceinline__ void lin_codes_to_tmem(uint32_t src, uint32_t taddr) 
 
 // ------------------------------------------------------------- scheduling --
 
+// linear_kernel is launched with programmatic stream serialization: a block
+// lets the next kernel's blocks take the SMs as they come free (every block of
+// this one is running by then), and before its first access to memory that
+// another kernel may have written, or may still read, it waits until all kernels
+// before it are done and their writes visible.  What precedes is only a block's
+// own preparation (barriers, tensor memory).
+__device__ __forceinline__ void lin_release_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void lin_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // A unit of work: one tile of 128 weight rows by up to NT consecutive rows of X
 // of one expert.
 struct LinUnit {
@@ -460,6 +469,7 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
     const uint32_t split = 1u << P.log_split, rank = blockIdx.x & (split - 1u);
     const uint32_t index = blockIdx.x >> P.log_split;      // unit: token tile by row tile, row tiles fastest
     if (warp == 2) {
+        lin_wait_previous();
         const uint32_t tt = index / (uint32_t)P.rts;
         LinUnit u = lin_find<NT>(P, (int)tt);
         u.rt = (int32_t)(index - tt * (uint32_t)P.rts);
@@ -488,6 +498,8 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
+    lin_wait_previous();
+    lin_release_next();
     const LinUnit u = s_unit;
     const int mv = u.m1 - u.m0;                            // rows of X in the unit
     // this block's column blocks, two a stage
@@ -741,10 +753,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.tmap_x)) : "memory");
     }
-    const int tts = lin_total<kPairNT>(P);                 // token tiles
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     lin_cluster_sync();                                    // the other block's barriers are ready
+    const int tts = lin_total<kPairNT>(P);                 // token tiles
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
