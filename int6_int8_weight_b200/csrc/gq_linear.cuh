@@ -120,10 +120,32 @@ struct LinEpi {
     int32_t bias_bf16, residual_bf16, y_bf16, act;
 };
 
-// N values through the activation, in place.  silu and the tanh form of gelu
-// (z * sigmoid(2 w)) take the exponential and the quotient from the special
-// function unit: a few units in the last place of a factor at most 1.  NaN
-// stays NaN.
+// 1 / (1 + 2^a), from the special function unit: 0 and 1 where 2^a over- or
+// underflows.
+__device__ __forceinline__ float lin_sigmoid2(float a) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
+// The normal distribution function: 1 - Phi(|x|) = t (b1 + t (b2 + .. + t b5)) e^(-x^2 / 2), t = 1 / (1 + q |x|), the
+// approximation of Hastings (Abramowitz and Stegun 7.1.26, with half its coefficients), absolute error below 1e-7.
+__device__ __forceinline__ float lin_phi(float x) {
+    float t, e;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(__fmaf_rn(0.23164189f, fabsf(x), 1.0f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * x * -0.72134752f));
+    float p = __fmaf_rn(t, 0.5307027145f, -0.7265760135f);
+    p = __fmaf_rn(t, p, 0.7107068705f);
+    p = __fmaf_rn(t, p, -0.142248368f);
+    p = __fmaf_rn(t, p, 0.127414796f);
+    p = p * t * e;
+    return x < 0.0f ? p : 1.0f - p;
+}
+
+// N values through the activation, in place.  silu and the gelus
+// take the exponential and the quotient from the special function unit: a few
+// units in the last place of a factor at most 1.  NaN stays NaN.
 template <int N>
 __device__ __forceinline__ void lin_act(float (&z)[N], int act) {
     // one test of `act` for all of them, and a loop of its own for each
@@ -135,12 +157,12 @@ __device__ __forceinline__ void lin_act(float (&z)[N], int act) {
         case GQ_ACT_RELU: each([](float x) { return x < 0.0f ? 0.0f : x; }); break;
         case GQ_ACT_RELU2: each([](float x) { x = x < 0.0f ? 0.0f : x; return x * x; }); break;
         case GQ_ACT_LEAKY_RELU2: each([](float x) { x = x < 0.0f ? 0.5f * x : x; return x * x; }); break;
-        case GQ_ACT_SILU: each([](float x) { return __fdividef(x, 1.0f + __expf(-x)); }); break;
-        case GQ_ACT_GELU: each([](float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f)); }); break;
+        case GQ_ACT_SILU: each([](float x) { return x * lin_sigmoid2(-1.4426950408889634f * x); }); break;
+        case GQ_ACT_GELU: each([](float x) { return x * lin_phi(x); }); break;
         case GQ_ACT_GELU_TANH:
+            // tanh(w) + 1 = 2 sigmoid(2 w), 2 w = 2 sqrt(2 / pi) (x + 0.044715 x^3), here times -log2(e)
             each([](float x) {
-                const float w = 1.5957691216057308f * __fmaf_rn(0.044715f * x, x * x, x);
-                return __fdividef(x, 1.0f + __expf(-w));
+                return x * lin_sigmoid2(x * __fmaf_rn(x * x, -0.10294324f, -2.3022082f));
             });
             break;
         default: break;
@@ -152,15 +174,15 @@ __device__ __forceinline__ float lin_elem(const void* p, int64_t i, int bf16) {
 }
 
 // N rows of Y from row m on, column n (the first `count` of them), from their
-// sums, the column's scale and bias.  The residual is read before anything is
-// written (it may be Y itself), all N loads in flight while the activation is
-// worked out.  Whole runs are told apart from the last rows of a tile: a test
-// and a branch for each element cost as much as the rest.
-template <bool WHOLE, int N>
+// sums, the column's scale and bias.  The residual (RES: there is one) is read
+// before anything is written (it may be Y itself), all N loads in flight while the
+// activation is worked out.  Whole runs are told apart from the last rows of a
+// tile: a test and a branch for each element cost as much as the rest.
+template <bool RES, bool WHOLE, int N>
 __device__ __forceinline__ void lin_rows_out(const LinEpi& E, float (&v)[N], int count, float s, float b, int64_t m,
                                              int64_t n) {
     uint32_t r[N];
-    if (E.residual) {
+    if constexpr (RES) {
         if (E.residual_bf16) {
             const uint16_t* p = static_cast<const uint16_t*>(E.residual) + m * E.ldr + n;
 #pragma unroll
@@ -172,13 +194,9 @@ __device__ __forceinline__ void lin_rows_out(const LinEpi& E, float (&v)[N], int
         }
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= s;
-    if (E.bias) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += b;
-    }
+    for (int i = 0; i < N; ++i) v[i] = __fmaf_rn(v[i], s, b);   // (b is 0 without a bias)
     lin_act(v, E.act);
-    if (E.residual) {
+    if constexpr (RES) {
         const int shift = E.residual_bf16 ? 16 : 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __uint_as_float(r[i] << shift);
@@ -196,11 +214,18 @@ __device__ __forceinline__ void lin_rows_out(const LinEpi& E, float (&v)[N], int
     }
 }
 
+template <bool RES, int N>
+__device__ __forceinline__ void lin_finish_as(const LinEpi& E, float (&v)[N], int count, float s, float b, int64_t m,
+                                           int64_t n) {
+    if (count >= N) lin_rows_out<RES, true>(E, v, count, s, b, m, n);
+    else lin_rows_out<RES, false>(E, v, count, s, b, m, n);
+}
+
 template <int N>
 __device__ __forceinline__ void lin_finish(const LinEpi& E, float (&v)[N], int count, float s, float b, int64_t m,
                                            int64_t n) {
-    if (count >= N) lin_rows_out<true>(E, v, count, s, b, m, n);
-    else lin_rows_out<false>(E, v, count, s, b, m, n);
+    if (E.residual) lin_finish_as<true>(E, v, count, s, b, m, n);
+    else lin_finish_as<false>(E, v, count, s, b, m, n);
 }
 
 struct LinParams {
@@ -753,10 +778,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.tmap_x)) : "memory");
     }
+    const int tts = lin_total<kPairNT>(P);                 // token tiles
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     lin_cluster_sync();                                    // the other block's barriers are ready
-    const int tts = lin_total<kPairNT>(P);                 // token tiles
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
@@ -862,10 +887,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 turn = false;
                 --left;
                 if (n < P.N && c < mv) {                   // (the residual is in L2: the copying warp asked for it)
-                    float z[16];
+                    // 16 rows at once, or eight with a residual, whose loads take as many registers: each form on its own
+                    // keeps within them (one for both: 399 us for 369, M 4096, N = K = 8192)
+                    if (P.epi.residual) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) z[i] = v[i >> 2][i & 3];
-                    lin_finish(P.epi, z, mv - c, sc, bi, (int64_t)m0 + c, n);
+                        for (int h = 0; h < 16; h += 8) {
+                            if (c + h >= mv) break;
+                            float z[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) z[i] = v[(h + i) >> 2][i & 3];
+                            lin_finish_as<true>(P.epi, z, mv - c - h, sc, bi, (int64_t)m0 + c + h, n);
+                        }
+                    } else {
+                        float z[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) z[i] = v[i >> 2][i & 3];
+                        lin_finish_as<false>(P.epi, z, mv - c, sc, bi, (int64_t)m0 + c, n);
+                    }
                 }
                 c += 64;
 #pragma unroll
