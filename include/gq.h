@@ -472,7 +472,8 @@ GQ_API gq_status gq_gemm_fakequant(const void* d_x, int64_t M, int64_t K, int64_
  * act(bias) + residual.  No workspace; Y is the same bits on every call with
  * the same arguments (no atomics: a K range split over blocks is summed in a
  * fixed order).  |Z - exact| <= (K/8 + 32) * 2^-24 * sum_k |X * W| plus one
- * binary32 rounding for the scale and one for the bias.
+ * binary32 rounding for scale and bias together; silu and the gelus are good to
+ * a few units in the last place of max(|z|, 1).
  * NaN and infinities of X, bias and residual propagate as in those formulas
  * (relu(NaN) = NaN).
  *
@@ -541,7 +542,9 @@ GQ_API gq_status gq_gemm_grouped(const void* d_x, int64_t M, int64_t K, int64_t 
  * u1, u2 are 16 random bits each (k * 2^-16) from a hash of the element's
  * index, the tensor's place in the batch, the step and the seed: rounding is
  * unbiased, so that changes of a state smaller than a code's step are not
- * lost, and reproducible.
+ * lost, and reproducible.  (An m far below its block's largest is stored as 0
+ * or as a whole code step, the mean being right: such an element moves seldom
+ * and then by more than the 32-bit step would move it.)
  *
  * t[i]: p (fp32 / bf16), g (fp32 / bf16), m, v dense arrays of numel elements;
  * m_scale, v_scale [ceil(numel / 256)] for 8-bit states, else NULL; p_copy

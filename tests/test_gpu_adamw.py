@@ -43,8 +43,9 @@ def _f4(q):
     return t * t
 
 
-def reference(p, g, m, v, ms, vs, step, seed, tensor, wd, lr, b1, b2, eps, grad_scale=None):
-    """One tensor's step in binary32 (numpy arrays in, new ones out; p fp32, rounded by the caller for bf16)."""
+def reference(p, g, m, v, ms, vs, step, seed, tensor, wd, lr, b1, b2, eps, grad_scale=None, first=0):
+    """One tensor's step in binary32 (numpy arrays in, new ones out; p fp32, rounded by the caller for bf16);
+    `first`: the index of their first element, a multiple of 256."""
     n = len(p)
     if grad_scale is not None:
         g = g * F(grad_scale)
@@ -58,7 +59,7 @@ def reference(p, g, m, v, ms, vs, step, seed, tensor, wd, lr, b1, b2, eps, grad_
     if ms is None:
         return p, m, v, None, None
     key = (seed + step * 0x632BE5AB + tensor * 0x2C1B3C6D) & 0xFFFFFFFF
-    z = _blocks(_hash(np.arange(n, dtype=np.uint64), key))
+    z = _blocks(_hash(np.arange(first, first + n, dtype=np.uint64), key))
     um, uv = (z >> np.uint64(16)).astype(F) * F(2.0 ** -16), (z & np.uint64(0xFFFF)).astype(F) * F(2.0 ** -16)
     mb, vb = _blocks(m), _blocks(v)
     am, av = np.abs(mb).max(1), vb.max(1)
@@ -254,6 +255,46 @@ def test_rounding_of_states_is_unbiased(gq):
     assert codes.max().item() == k + 1
     assert abs(got_m - m_true) <= 5 * step_m / (2 * 64) + 1e-6 * m_true
     assert abs(got_v - v_true) <= 5 * step_v / (2 * 64) + 1e-6 * v_true
+
+
+def test_more_elements_than_32_bits_count(gq):
+    """2^32 + 700 elements: the last blocks, whose index needs the hash's high word, against the reference."""
+    n, tail = (1 << 32) + 700, 700 + 512
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    m, v = torch.zeros(n, dtype=torch.int8, device="cuda"), torch.zeros(n, dtype=torch.uint8, device="cuda")
+    sc = [torch.zeros(-(-n // BLOCK), device="cuda") for _ in range(2)]
+    rng = np.random.default_rng(4)
+    g[-tail:] = torch.from_numpy(rng.standard_normal(tail).astype(F)).cuda()
+    gq.adamw_step([p], [g], [m], [v], step=1, scales=([sc[0]], [sc[1]]), seed=9, weight_decay=0.0, **HYPER)
+    zero = np.zeros(-(-tail // BLOCK), F)
+    w, qm, qv, ms, vs = reference(np.zeros(tail, F), g[-tail:].float().cpu().numpy(), np.zeros(tail, np.int8),
+                                  np.zeros(tail, np.uint8), zero, zero, 1, 9, 0, 0.0, HYPER["lr"], 0.9, 0.95, 1e-8,
+                                  first=n - tail)
+    assert torch.equal(p[-tail:].cpu(), _bf16(w))
+    assert np.array_equal(m[-tail:].cpu().numpy(), qm) and np.array_equal(v[-tail:].cpu().numpy(), qv)
+    assert np.array_equal(sc[0][-len(ms):].cpu().numpy(), ms) and np.array_equal(sc[1][-len(vs):].cpu().numpy(), vs)
+    assert not m[:1 << 20].any() and not sc[0][:1000].any()
+
+
+def test_mixed_state_sizes_in_one_call(gq):
+    """The C entry takes 8-bit and 32-bit states in one batch; a tensor's place in it keeps its random bits."""
+    A, B = Tensors([300, 5000], bits=8, seed=1), Tensors([700], bits=32, seed=2)
+    before = A.host()[:1] + B.host() + A.host()[1:]
+    order = [(A, 0), (B, 0), (A, 1)]
+    arr = (gq.GQAdamWTensor * 3)()
+    for d, (T, i) in zip(arr, order):
+        d.p, d.g, d.m, d.v, d.numel = (T.p[i].data_ptr(), T.g[i].data_ptr(), T.m[i].data_ptr(), T.v[i].data_ptr(),
+                                       T.p[i].numel())
+        d.state_bits, d.weight_decay = T.bits, 0.01
+        if T.bits == 8:
+            d.m_scale, d.v_scale = T.scales[0][i].data_ptr(), T.scales[1][i].data_ptr()
+    h = gq.GQAdamWHyper(lr=HYPER["lr"], beta1=0.9, beta2=0.95, eps=1e-8, step=7, seed=11)
+    assert gq.LIB.gq_adamw_step(arr, 3, h, torch.cuda.current_stream().cuda_stream) == 0
+    for k, ((T, i), b) in enumerate(zip(order, before)):
+        p, m, v, ms, vs = reference(*b, 7, 11, k, 0.01, HYPER["lr"], 0.9, 0.95, 1e-8)
+        assert np.array_equal(T.p[i].cpu().numpy(), p) and np.array_equal(T.m[i].cpu().numpy(), m)
+        assert np.array_equal(T.v[i].cpu().numpy(), v)
 
 
 def test_refusals(gq):

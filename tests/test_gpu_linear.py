@@ -192,6 +192,18 @@ def test_epilogue(gq, M, act, bias, residual, out):
     _run(gq, M, 272, 384, 6, act, bias, residual, out)
 
 
+# Many rows and enough columns that the tiles go over pairs of SMs: odd and ragged sizes, odd counts of column blocks,
+# more units than pairs.
+@pytest.mark.parametrize("qbits", [6, 8])
+@pytest.mark.parametrize("M,N,K,act,bias,residual,out", [
+    (500, 5700, 1544, "none", "none", "none", torch.float32), (257, 8191, 1601, "silu", "bf16", "bf16", torch.bfloat16),
+    (1100, 8192, 1536, "gelu", "f32", "f32", torch.bfloat16), (300, 8200, 2048, "gelu_tanh", "f32", "bf16", torch.float32),
+    (97, 12000, 1600, "relu2", "none", "f32", torch.float32), (2500, 2050, 1664, "leaky_relu2", "bf16", "bf16", torch.bfloat16),
+])
+def test_many_rows(gq, M, N, K, qbits, act, bias, residual, out):
+    _run(gq, M, N, K, qbits, act, bias, residual, out)
+
+
 def test_more_rows_than_one_wave(gq):
     """Enough tiles that every block takes several."""
     _run(gq, 3000, 4096, 128, 6, "silu", "bf16", "bf16")
@@ -227,12 +239,12 @@ def test_residual_in_place(gq):
 def test_special_values_propagate(gq):
     """NaN and infinities in a row of X reach that row's outputs and no other's."""
     rng = np.random.default_rng(9)
-    W = Weight(gq, rng, 1, 300, 200, 6)
-    t = gq.tile_weight(W.packed[0], 200, 6)
-    for M in (4, 70, 300):
-        x = _x(rng, M, 200)
+    for M, N, K in ((4, 300, 200), (70, 300, 200), (300, 300, 200), (300, 5700, 1540)):
+        W = Weight(gq, rng, 1, N, K, 6)
+        t = gq.tile_weight(W.packed[0], K, 6)
+        x = _x(rng, M, K)
         clean = gq.gemm_epilogue(x, t, W.scale[0], 6, act="relu")
-        x2 = x.clone()
+        x2 = _x(rng, M, K).copy_(x)                            # (a clone's rows would not start on 16 bytes)
         x2[1, 7], x2[2, 5] = float("nan"), float("inf")
         y = gq.gemm_epilogue(x2, t, W.scale[0], 6, act="relu")
         q0 = W.w[0][:, 5] == 0
@@ -243,7 +255,34 @@ def test_special_values_propagate(gq):
         assert torch.equal(y[keep], clean[keep])
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 512, 4096), (24, 700, 2048), (300, 512, 640)])
+@pytest.mark.parametrize("act,at", [("silu", -np.inf), ("gelu", np.inf), ("gelu_tanh", np.inf), ("relu", np.inf),
+                                    ("silu", 1e30), ("gelu", -1e30), ("gelu_tanh", -1e30), ("gelu", 40.0),
+                                    ("silu", -80.0), ("gelu_tanh", -30.0), ("relu2", -np.inf), ("leaky_relu2", -np.inf)])
+def test_activations_far_out(gq, act, at):
+    """Where the exponential over- or underflows: the formula's value."""
+    W = Weight(gq, np.random.default_rng(3), 1, 40, 64, 8)
+    x = torch.zeros((5, 64), dtype=torch.bfloat16, device="cuda")
+    b = torch.full((40,), at, device="cuda")
+    y = gq.gemm_epilogue(x, gq.tile_weight(W.packed[0], 64, 8), W.scale[0], 8, bias=b, act=act, out_dtype=torch.float32)
+    z = torch.tensor(at, dtype=torch.float64)
+    if act == "silu":
+        want = z / (1 + torch.exp(-z))
+    elif act == "gelu":
+        want = 0.5 * z * (1 + torch.erf(z * 0.5 ** 0.5))
+    elif act == "gelu_tanh":
+        want = 0.5 * z * (1 + torch.tanh((2 / np.pi) ** 0.5 * (z + 0.044715 * z ** 3)))
+    else:
+        want = _act64(z, act)
+    want = float(want)
+    if np.isnan(want):
+        assert y.isnan().all()
+    elif np.isinf(want):
+        assert (y == want).all()
+    else:
+        assert (y.double() - want).abs().max() <= 16 * 2.0 ** -24 * max(abs(want), 1.0)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 512, 4096), (24, 700, 2048), (300, 512, 640), (300, 8192, 1600)])
 def test_same_bits_every_time(gq, M, N, K):
     """No atomics: the same call gives the same bits, eager, on another stream and replayed from a graph."""
     rng = np.random.default_rng(10)
@@ -271,6 +310,80 @@ def test_same_bits_every_time(gq, M, N, K):
         g1.replay(), g2.replay()
         torch.cuda.synchronize()
         assert torch.equal(y1, want) and torch.equal(y2, want)
+
+
+def test_two_streams_at_once(gq):
+    """Calls of both kernels that run side by side do not disturb each other."""
+    rng = np.random.default_rng(14)
+    jobs = []
+    for M, N, K in ((3, 640, 4096), (200, 1000, 1024), (300, 6000, 1536)):
+        W = Weight(gq, rng, 1, N, K, 6)
+        t, x = gq.tile_weight(W.packed[0], K, 6), _x(rng, M, K)
+        jobs.append((x, t, W.scale[0], gq.gemm_epilogue(x, t, W.scale[0], 6, act="silu")))
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    got = [[] for _ in jobs]
+    for _ in range(20):
+        for (x, t, s, _), st, g in zip(jobs, streams, got):
+            with torch.cuda.stream(st):
+                g.append(gq.gemm_epilogue(x, t, s, 6, act="silu"))
+    torch.cuda.synchronize()
+    for (_, _, _, want), g in zip(jobs, got):
+        assert all(torch.equal(y, want) for y in g)
+
+
+def test_a_row_of_dependent_calls(gq):
+    """Each call reads what the one before wrote (their blocks may overlap in time), eager and captured."""
+    rng = np.random.default_rng(15)
+    Ws = [Weight(gq, rng, 1, 512, 512, 6) for _ in range(3)]
+    ts = [gq.tile_weight(W.packed[0], 512, 6) for W in Ws]
+    for M in (1, 40, 130):
+        x0 = _x(rng, M, 512)
+
+        def chain(x):
+            for _ in range(10):
+                for W, t in zip(Ws, ts):
+                    x = gq.gemm_epilogue(x, t, W.scale[0], 6, act="silu", residual=x)
+            return x
+
+        x = x0
+        for _ in range(10):
+            for W, t in zip(Ws, ts):
+                x = gq.gemm_epilogue(x, t, W.scale[0], 6, act="silu", residual=x)
+                torch.cuda.synchronize()
+        assert torch.equal(chain(x0), x)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = chain(x0)
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, x)
+
+
+def test_offsets_past_32_bits(gq):
+    """Y of more than 2^31 elements, and experts' codes past 2^31 bytes."""
+    rng = np.random.default_rng(16)
+    W = Weight(gq, rng, 1, 16400, 64, 6)
+    x = _x(rng, 131200, 64)
+    y = gq.gemm_epilogue(x, gq.tile_weight(W.packed[0], 64, 6), W.scale[0], 6, act="relu")
+    for s in (slice(0, 100), slice(131100, 131200)):
+        _check(y[s], x[s], W.w[0], None, None, "relu", s)
+    del y, x
+    E, N, K = 34, 8192, 8192
+    nbytes = gq.LIB.gq_tile_bytes(N, K, 8)
+    assert E * nbytes > 1 << 31
+    W = Weight(gq, rng, 1, N, K, 8)
+    tiles = torch.zeros((E, nbytes), dtype=torch.uint8, device="cuda")
+    tiles[E - 1] = gq.tile_weight(W.packed[0], K, 8)
+    scale = torch.zeros((E, N), dtype=torch.float16, device="cuda")
+    scale[E - 1] = W.scale[0]
+    for M in (6, 3500):
+        x = _x(rng, M, K)
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[E] = M
+        y = gq.gemm_grouped(x, off, tiles, scale, 8)
+        _check(y[-50:], x[-50:], W.w[0], None, None, "none", M)
 
 
 # ----------------------------------------------------------------- grouped --
@@ -302,6 +415,13 @@ def test_grouped(gq, counts, N, K, qbits):
     _grouped(gq, counts, N, K, qbits)
 
 
+@pytest.mark.parametrize("qbits", [6, 8])
+@pytest.mark.parametrize("counts", [[200, 0, 257, 31, 600, 1], [128] * 9, [0, 0, 900, 0]])
+def test_grouped_many_rows(gq, counts, qbits):
+    """Over pairs of SMs: ragged, empty and lone experts, a padded batch."""
+    _grouped(gq, counts, 2500, 1600, qbits, "gelu", "f32", "bf16", torch.bfloat16, first=2, behind=40)
+
+
 @pytest.mark.parametrize("act", ["silu", "leaky_relu2"])
 @pytest.mark.parametrize("counts", [[1, 0, 2], [30, 200, 0, 3]])
 def test_grouped_epilogue_and_padding(gq, counts, act):
@@ -311,15 +431,20 @@ def test_grouped_epilogue_and_padding(gq, counts, act):
 def test_grouped_bad_offsets_are_reported(gq):
     """Offsets outside the batch or descending: a status, no write outside Y."""
     rng = np.random.default_rng(11)
-    W = Weight(gq, rng, 3, 140, 128, 6)
-    tiles, x = gq.tile_weight(W.packed, 128, 6), _x(rng, 50, 128)
-    for off in ([0, 10, 5, 50], [-4, 10, 20, 50], [0, 20, 51, 51], [0, 1 << 30, 1 << 30, 1 << 30],
-                [-(1 << 31), -5, -1, 2]):
-        pad = torch.full((52, 140), 7.0, dtype=torch.bfloat16, device="cuda")
-        with pytest.raises(gq.GQError, match="0x8"):
-            gq.gemm_grouped(x, torch.tensor(off, dtype=torch.int32, device="cuda"), tiles, W.scale, 6, y=pad[1:51],
-                            check_status=True)
-        assert (pad[0] == 7).all() and (pad[51] == 7).all()
+    for N, K, M in ((140, 128, 50), (4100, 1600, 650)):        # the second over pairs of SMs
+        W = Weight(gq, rng, 3, N, K, 6)
+        tiles, x = gq.tile_weight(W.packed, K, 6), _x(rng, M, K)
+        for off in ([0, 10, 5, M], [-4, 10, 20, M], [0, 20, M + 1, M + 1], [0, 1 << 30, 1 << 30, 1 << 30],
+                    [-(1 << 31), -5, -1, 2], [0, M, 0, M]):
+            pad = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device="cuda")
+            with pytest.raises(gq.GQError, match="0x8"):
+                gq.gemm_grouped(x, torch.tensor(off, dtype=torch.int32, device="cuda"), tiles, W.scale, 6,
+                                y=pad[1:M + 1], check_status=True)
+            assert (pad[0] == 7).all() and (pad[M + 1] == 7).all()
+    W = Weight(gq, rng, 70, 64, 64, 6)                         # a bad offset behind every row's expert
+    off = torch.tensor([0] + [5] * 69 + [4], dtype=torch.int32, device="cuda")
+    with pytest.raises(gq.GQError, match="0x8"):
+        gq.gemm_grouped(_x(rng, 5, 64), off, gq.tile_weight(W.packed, 64, 6), W.scale, 6, check_status=True)
 
 
 def test_grouped_equals_single_weights(gq):
