@@ -57,6 +57,7 @@ extern "C" gq_status gq_adamw_step(const gq_adamw_tensor* t, int n, const gq_ada
     P.c2 = (float)(1.0 - h->beta2);
     P.eps = (float)h->eps;
     P.one = 1.0f;
+    P.paired = P.eps <= kAdamHigh / 4.0f;
     P.inv_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h->beta2, (double)step)));
     P.step_size = (float)(h->lr / P.bias1);
     P.key_step = (uint32_t)step * kAdamStepMul;

@@ -22,6 +22,7 @@ namespace gq {
 constexpr int kAdamDesc = 200;            // tensors a launch (the parameter block stays below 32 KB)
 constexpr int kAdamThreads = 256;
 constexpr int kAdamItem = 8 * kAdamThreads;
+constexpr float kAdamLow = 8.673617379884035e-19f, kAdamHigh = 1.152921504606847e18f;   // 2^-60, 2^60
 constexpr float kAdamTiny = 8.271806125530277e-25f;   // 2^-80: blocks below it store 0
 
 struct AdamDesc {
@@ -51,6 +52,7 @@ struct AdamParams {
     float inv_bc2;        // RN(1 / sqrt(1 - b2^t))
     float step_size;      // RN(lr / (1 - b1^t))
     float one;            // 1
+    int32_t paired;       // eps is in the paired quotient's range: sqrt(v) inv_bc2 + eps is too
     const int64_t* d_step;
     const float* d_lr;
     const float* d_grad_scale;
@@ -108,6 +110,37 @@ struct AdamOne {
         return r;
     }
 };
+// Square root and quotient of pairs, correctly rounded, by Newton steps on the
+// special function unit's estimates with exact residuals (Markstein): for the
+// root r of v, v - r^2 decides the last bit; for the quotient q of m and d,
+// m - d q, times a correctly rounded reciprocal.  The residuals are exact, and
+// so the results those of the IEEE operations, while nothing under- or
+// overflows: 2^-60 <= v <= 2^60, 2^-60 <= |d| <= 2^60, 2^-60 <= |m| <= 2^60.
+// (Checked against the IEEE operations for every significand of v with both
+// parities of the exponent, every significand of d's reciprocal, and 2^33
+// quotients.)  11 instructions for an element against 22 for the IEEE operations,
+// which test every operand by themselves.
+__device__ __forceinline__ AdamF2 adam2_sqrt(AdamF2 v) {
+    float v0, v1, y0, y1;
+    adam2_out(v, v0, v1);
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(v0));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(v1));
+    const AdamF2 y = adam2(y0, y1), g = adam2_mul(v, y), h = adam2_mul(y, adam2(-0.5f));   // v^(1/2), -v^(-1/2) / 2
+    const AdamF2 e = adam2_fma(g, h, adam2(0.5f));
+    const AdamF2 g1 = adam2_fma(g, e, g), h1 = adam2_fma(h, e, h);
+    return adam2_fma(adam2_fma(g1, g1, adam2_mul(v, adam2(-1.0f))), h1, g1);
+}
+__device__ __forceinline__ AdamF2 adam2_div(AdamF2 m, AdamF2 d) {
+    float d0, d1, y0, y1;
+    adam2_out(d, d0, d1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(d0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(d1));
+    const AdamF2 nd = adam2_mul(d, adam2(-1.0f)), y = adam2(y0, y1);
+    const AdamF2 r = adam2_fma(y, adam2_fma(nd, y, adam2(1.0f)), y);    // RN(1 / d)
+    const AdamF2 q = adam2_mul(m, r), q1 = adam2_fma(adam2_fma(nd, q, m), r, q);
+    return adam2_fma(adam2_fma(nd, q1, m), r, q1);
+}
+
 // f(q) = RN((q^2)^2); q^2 is exact.
 __device__ __forceinline__ AdamF2 adam2_fourth(AdamF2 q) {
     const AdamF2 t = adam2_mul(q, q);
@@ -280,11 +313,38 @@ __global__ void __launch_bounds__(kAdamThreads, S8 ? 5 : 4) adamw_kernel(const _
                                     adam2_mul(adam2_mul(g2, g2), adam2(P.c2)));
             adam2_out(m2, m[i], m[i + 1]);
             adam2_out(v2, v[i], v[i + 1]);
-            const AdamF2 r2 = adam2(__fsqrt_rn(v[i]), __fsqrt_rn(v[i + 1]));
-            float d0, d1;
-            adam2_out(U.add(adam2_mul(r2, adam2(inv_bc2)), adam2(P.eps)), d0, d1);
-            const AdamF2 u2 = adam2_mul(adam2(__fdiv_rn(m[i], d0), __fdiv_rn(m[i + 1], d1)), adam2(step_size));
-            adam2_out(U.sub(adam2_mul(adam2(p[i], p[i + 1]), adam2(decay)), u2), p[i], p[i + 1]);
+        }
+        // p' = p decay - (m / (sqrt(v) inv_bc2 + eps)) step_size.  32-bit states wait for memory and take the IEEE
+        // operations; so do lanes whose values leave the range of the paired ones.
+        float am = 0.0f, av = 0.0f;                        // (past the tensor's end m and v are 0)
+        bool plain = !S8;
+        if constexpr (S8) {
+            float lo_m = fabsf(m[0]), lo_v = v[0];
+            am = lo_m;
+            av = lo_v;
+#pragma unroll
+            for (int i = 1; i < 8; ++i) {
+                lo_m = fminf(lo_m, fabsf(m[i]));
+                lo_v = fminf(lo_v, v[i]);
+                am = fmaxf(am, fabsf(m[i]));
+                av = fmaxf(av, v[i]);
+            }
+            // (a NaN, which min and max pass over, comes out of either form as a NaN)
+            plain = !(fminf(lo_m, lo_v) >= kAdamLow && fmaxf(am, av) <= kAdamHigh) || !P.paired;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            AdamF2 u2;
+            if (plain) {
+                const AdamF2 r2 = adam2(__fsqrt_rn(v[i]), __fsqrt_rn(v[i + 1]));
+                float d0, d1;
+                adam2_out(U.add(adam2_mul(r2, adam2(inv_bc2)), adam2(P.eps)), d0, d1);
+                u2 = adam2(__fdiv_rn(m[i], d0), __fdiv_rn(m[i + 1], d1));
+            } else {
+                u2 = adam2_div(adam2(m[i], m[i + 1]), U.add(adam2_mul(adam2_sqrt(adam2(v[i], v[i + 1])), adam2(inv_bc2)),
+                                                            adam2(P.eps)));
+            }
+            adam2_out(U.sub(adam2_mul(adam2(p[i], p[i + 1]), adam2(decay)), adam2_mul(u2, adam2(step_size))), p[i], p[i + 1]);
         }
         adam_store(p, D.p, e, n, pb, vec);
         if (D.copy) adam_store(p, D.copy, e, n, true, vec);
@@ -292,14 +352,6 @@ __global__ void __launch_bounds__(kAdamThreads, S8 ? 5 : 4) adamw_kernel(const _
             adam_store(m, D.m, e, n, false, vec);
             adam_store(v, D.v, e, n, false, vec);
             continue;
-        }
-        // past the tensor's end m and v are 0: they do not raise the maxima
-        float am = 0.0f, av = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i >= n) m[i] = v[i] = 0.0f;
-            am = fmaxf(am, fabsf(m[i]));
-            av = fmaxf(av, v[i]);
         }
         am = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(am)));   // non-negative: ordered like their bits
         av = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(av)));
