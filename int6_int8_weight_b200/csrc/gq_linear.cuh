@@ -311,6 +311,13 @@ __device__ __forceinline__ void lin_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// g_wait with its first test kept apart from the loop: what follows a wait that
+// is over at once is a branch (the ALU is what the conversion is bound by).
+__device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity) {
+    if (__builtin_expect(g_try_wait(bar, parity), 1)) return true;
+    return g_wait(bar, parity);
+}
+
 // One weight row's 64 codes of a block (its 16-byte chunks lie 2048 bytes apart
 // at shared address `src`) into the 32 TMEM columns at `taddr` of this
 // thread's lane: column j holds k = 2j and 2j + 1 as bf16.
@@ -601,7 +608,8 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
             // The slot first: once stage i - slots is done, stage i - stages (no later, the ring being at least as deep)
             // has landed, so a parity test of full(s) cannot take an older phase for this one; nor can one of
             // tfree(t), since the group's last stage was at most `slots` before.
-            if ((i >= (int)S::slots && !g_wait_warp(tfree(t), tph ^ 1u)) || !g_wait_warp(full(s), ph)) {
+            if ((i >= (int)S::slots && !lin_wait(tfree(t), tph ^ 1u)) || !lin_wait(full(s), ph)) ok = false;
+            if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
