@@ -59,11 +59,12 @@
  *    bytes]); the input may be strided (ld >= cols elements).
  *  - A tensor with rows == 0 or cols == 0 is a no-op; its pointers may be NULL.
  *  - No call synchronizes with the host, traps or asserts on the device.  The
- *    only waits on the device are the fused row kernel's waits for its own
- *    bulk copies into shared memory (and its consumers' waits for one
- *    another); each gives up after about 4 s of %globaltimer, drains the
- *    copies still in flight (again bounded), sets GQ_STATUS_TIMEOUT in the
- *    descriptor's status word and lets the launch end.
+ *    only waits on the device are waits of the fused row kernel and of the
+ *    products for their own copies into shared memory and their own matrix
+ *    instructions, and of warps of a block, or of the few blocks of a cluster,
+ *    for one another; each gives up after about 4 s of %globaltimer, drains
+ *    the copies still in flight (again bounded), sets GQ_STATUS_TIMEOUT in the
+ *    status word and lets the launch end.
  */
 #ifndef GQ_H
 #define GQ_H
@@ -478,13 +479,16 @@ GQ_API gq_status gq_gemm_fakequant(const void* d_x, int64_t M, int64_t K, int64_
  * (relu(NaN) = NaN).
  *
  * gq_gemm_grouped is the same product with one weight per group of rows (the
- * experts of a mixture, their rows sorted by expert): rows d_offsets[e] .. 
+ * experts of a mixture, their rows sorted by expert): rows d_offsets[e] ..
  * d_offsets[e + 1] - 1 of X, residual and Y belong to expert e and use its
  * tiles, scale [E, N] and bias [E, N].  d_offsets is device int32 [E + 1],
  * non-decreasing in [0, M]; experts may have no row, and rows outside
  * [d_offsets[0], d_offsets[E]) are not written (a padded batch).  An offset
  * that decreases or lies outside [0, M] sets GQ_STATUS_OFFSETS and Y is then
  * unspecified within its M rows.  E <= 65535.
+ *
+ * Y overlaps no input of the call but a residual as said above.  A call may run
+ * beside others on other streams; nothing is shared between calls.
  * Source: the layers that consume the fake-quant weights, with the MLPs'
  * ReLU^2 and LeakyReLU^2 (slope 0.5) of the pages; PR #69, PR #1202, PR #1495.
  */
@@ -550,14 +554,15 @@ GQ_API gq_status gq_gemm_grouped(const void* d_x, int64_t M, int64_t K, int64_t 
  * m_scale, v_scale [ceil(numel / 256)] for 8-bit states, else NULL; p_copy
  * nullable: bf16 copy of p' (the model's weights when p is the fp32 master).
  * Pointers are aligned to their element size; 16-byte aligned ones take the
- * vector path.  numel 0 is a no-op.  h: host struct.
+ * vector path.  numel 0 is a no-op.  No array that the step writes may overlap
+ * another of the batch (a weight is listed once).  h: host struct.
  * d_step, d_lr (nullable, device): read by the kernel instead of h->step and
  * h->lr, so that a captured step can be replayed while both move on.
  * d_grad_scale nullable, device binary32 (loss unscaling, clipping).
  * A non-finite gradient reaches p, m and v as the formulas say (32-bit); in an
  * 8-bit block whose m' or v' has a NaN or an infinity the new codes and
  * scales of that block are unspecified.
- * Asynchronous on `stream`; one launch per 200 tensors of a state size.
+ * Asynchronous on `stream`, no workspace; one launch per 200 tensors of a state size.
  * Source: AdamW with decoupled weight decay (PR #69, PR #1414).
  */
 typedef struct gq_adamw_tensor {

@@ -2,11 +2,13 @@
 // 8 bits (the definition is in include/gq.h; every line of it is one binary32
 // rounding).
 //
-// Bound: HBM.  A step reads p, g, m, v and writes p, m, v once: 28 bytes per
-// element with fp32 weights and states, 10 with bf16 weights and 8-bit states.
-// The arithmetic (one IEEE square root and one IEEE division an element, and
-// for 8-bit states two fourth roots' worth of comparisons and a hash) is about
-// 60 / 110 instructions an element.
+// A step reads p, g, m, v and writes p, m, v once: 28 bytes per element with
+// fp32 weights and states, 10 with bf16 weights and 8-bit states.  Bound with
+// 32-bit states: HBM (the weights of 9 layers of d 512, 606 MB in all, in 93 us:
+// 6.5 TB/s).  With 8-bit states the square root, the quotient,
+// the fourth root and the hash come to about 90 instructions an element, and
+// their issue is the bound: 16384 x 8192 bf16 in 449 us, 3.0 TB/s, 70 % of the
+// issue slots.
 //
 // Split: a work item is a run of 2048 elements of one tensor (8 blocks of 256,
 // one a warp), so that any list of tensors spreads evenly; a lane owns 8

@@ -380,19 +380,24 @@ __device__ __forceinline__ void lin_cut(LinUnit& u, int a, int b, int j) {
     u.m1 = min(b - u.m0, step) + u.m0;
 }
 
-// Token tiles of the whole batch (one warp).
+// Token tiles of the whole batch (one warp): none where an offset is out of order or range, since ranges that overlap
+// could add up to any number of tiles.
 template <int NT>
 __device__ __forceinline__ int lin_total(const LinParams& P) {
     if (!P.offsets) return (int)((P.M + NT - 1) / NT);
     unsigned sum = 0;
+    bool ok = true;
     for (int e = threadIdx.x & 31; e < (int)P.E; e += 32) {
         const int p = __ldg(P.offsets + e), q = __ldg(P.offsets + e + 1);
         if (p >= 0 && q >= p && q <= (int)P.M)
             sum += ((unsigned)(q - p) + NT - 1u) / NT;
-        else if (P.status)
-            atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x8u);
+        else
+            ok = false;
     }
-    return (int)__reduce_add_sync(0xffffffffu, sum);
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (__all_sync(0xffffffffu, ok)) return (int)sum;
+    if (threadIdx.x == 0 && P.status) atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x8u);
+    return 0;
 }
 
 // The MMAs' N for a unit of the pair kernel: its rows in steps of 32.
@@ -687,12 +692,17 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
 // one block per tile: per SM and column block 16 KB of X and 6 KB of codes
 // against 512 cycles of MMAs.
 // Persistent: a pair takes every pairs-th unit.  TMEM: 256 columns of sums, 256
-// for four stages of A.  The conversion warps run ahead into the next unit by
-// those four stages (2048 cycles of MMAs), then drain the finished sums into
-// registers (which frees them for the next unit's MMAs), and only then apply the
-// epilogue and store, while the MMAs run on what was converted ahead.
-// Block 0's barriers gather both blocks' conversions (wready) and drains
-// (acc_empty); the MMAs' commits arrive on both blocks' barriers.
+// for four stages of A.  Warp 0 copies, warp 1 of block 0 issues the MMAs (2 and
+// 3 only make up the warpgroup that hands its registers over), 4 .. 19 convert,
+// four groups of four, group g the stages that are g modulo 4.  The groups convert
+// three stages ahead into the next unit (1500 cycles of MMAs), take the finished
+// sums into registers as soon as the last MMA is done (64 a thread; that frees
+// them for the next unit's MMAs), and apply the epilogue in four runs of 16
+// tokens, each between two stages of conversion, so that the MMAs never wait for
+// a whole epilogue.  Block 0's barriers gather both blocks' conversions (wready)
+// and drains (acc_empty); the MMAs' commits arrive on both blocks' barriers.
+// Bound: the tensor pipe.  M 4096, N = K = 8192, bias, gelu_tanh and residual: 370 us,
+// 499 thousand cycles where the MMAs alone take 459 thousand.
 constexpr int kPairNT = 256;
 constexpr int kPairThreads = 128 + 512;
 constexpr int kPairRoleRegs = 32, kPairConvRegs = 112;     // 4 * 32 + 16 * 112 = 20 * 96: what the block is launched with
@@ -878,7 +888,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int grp = (warp - 4) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         // Group grp takes the stages with seq % 4 == grp, so its TMEM slot is always the same.  (Everything that can be
-        // worked out again is: the drained sums take 64 of the 96 registers that 18 warps leave a thread.)
+        // worked out again is: the drained sums take 64 of a thread's 112 registers.)
         static_assert(kPairSlots == 4 && D >= 4, "the groups' slots; the ring is at least as deep");
         const uint32_t dst = tmem + lanes + kPairNT + 64u * grp;
         int next = grp, done = 0;                          // the group's next stage; units whose sums are drained
@@ -984,6 +994,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
 // K = 0: the sums are 0, the epilogue is all there is.  One block per row of Y.
 __global__ void __launch_bounds__(256) linear_empty_kernel(const __grid_constant__ LinParams P) {
+    if (P.offsets && P.status && blockIdx.x == 0)
+        for (int e = threadIdx.x; e < (int)P.E; e += blockDim.x) {
+            const int p = P.offsets[e], q = P.offsets[e + 1];
+            if (p < 0 || q < p || q > (int)P.M) atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x8u);
+        }
     for (int64_t m = blockIdx.x; m < P.M; m += gridDim.x) {
         int64_t e = 0;
         if (P.offsets) {                                   // the expert of the row: the last that begins at or before it

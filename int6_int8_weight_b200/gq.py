@@ -701,7 +701,7 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     [ceil(numel / 256)] (all zeros at the start); ``copies`` bf16 copies of the
     new weights (a list, entries may be None).  ``step`` (from 1) and ``lr`` are
     numbers, or int64 / fp32 tensors on the device that a captured step reads
-    when it is replayed.  ``weight_decay``: one number or one per tensor.
+    when it is replayed.  A weight is listed once.  ``weight_decay``: one number or one per tensor.
     ``grad_scale``: fp32 device tensor that multiplies every gradient.  ``seed``
     is that of the 8-bit states' rounding."""
     n = len(params)

@@ -10,9 +10,10 @@ Tolerances, element by element, before the last rounding:
 each for the scale and the bias).  An activation multiplies an error by its
 slope, at most S on the values in question (1 for none and relu, 2 |z| + A for
 the squares, 1.13 for silu and the two gelus), and its own binary32 steps err
-by at most 16 * 2^-24 of max(|z|, 1) (a handful of roundings; expf, erff and
-tanhf are good to 2 ulp; their arguments' errors pass through a slope below 1 per
-relative unit).  The residual adds one rounding 2^-24 |y|.  Y in bf16 adds half
+by at most 16 * 2^-24 of max(|z|, 1): a factor of at most 1 from the special
+function unit's exponential (2^-22 relative) and reciprocal (2^-23), the exponent's
+own rounding through z^2 s (1 - s) < 2, the normal distribution's approximation
+(1e-7, 2 * 2^-24), and a handful of roundings.  The residual adds one rounding 2^-24 |y|.  Y in bf16 adds half
 a step, 2^-8 |y| (2^-9 of the next power of two).
 """
 from __future__ import annotations
@@ -445,6 +446,24 @@ def test_grouped_bad_offsets_are_reported(gq):
     off = torch.tensor([0] + [5] * 69 + [4], dtype=torch.int32, device="cuda")
     with pytest.raises(gq.GQError, match="0x8"):
         gq.gemm_grouped(_x(rng, 5, 64), off, gq.tile_weight(W.packed, 64, 6), W.scale, 6, check_status=True)
+
+
+def test_grouped_bad_offsets_overlapping(gq):
+    """Expert ranges that overlap, each in order by itself: reported, and none of their tiles worked on by the pairs of
+    SMs (65535 experts of the whole batch would be as many products).  With no columns too."""
+    rng = np.random.default_rng(12)
+    E, M, N, K = 8, 1024, 2048, 1600
+    W = Weight(gq, rng, E, N, K, 8)
+    x, tiles = _x(rng, M, K), gq.tile_weight(W.packed, K, 8)
+    off = torch.tensor([0, M] * 4 + [0], dtype=torch.int32, device="cuda")
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(gq.GQError, match="0x8"):
+        gq.gemm_grouped(x, off, tiles, W.scale, 8, y=y, check_status=True)
+    assert (y == 7).all()
+    b = _extra(rng, "f32", E, N)
+    for o in (off, torch.tensor([0] * 8 + [M + 1], dtype=torch.int32, device="cuda")):
+        with pytest.raises(gq.GQError, match="0x8"):
+            gq.gemm_grouped(x[:, :0], o, tiles[:, :0], W.scale, 8, bias=b, check_status=True)
 
 
 def test_grouped_equals_single_weights(gq):
