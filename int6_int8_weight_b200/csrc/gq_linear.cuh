@@ -289,6 +289,37 @@ __device__ __forceinline__ float lin_ld_peer(uint32_t addr, uint32_t rank) {
     return f;
 }
 
+// The 4 MMAs (K = 16 each) of one column block, over CTAS blocks: as
+// g_mma_stage_ts, but from the low word of X's shared memory descriptor, and all
+// its arguments the same in every lane, so that the compiler can keep them in
+// uniform registers.  The issuing warp is the narrow place of a stage's way: with
+// descriptors put together anew for each column block M 16, N = K = 16384 takes
+// 43.7 us instead of 41.2.
+__device__ __forceinline__ uint32_t lin_desc_low(uint32_t addr) { return (uint32_t)g_smem_desc(addr); }
+template <int CTAS>
+__device__ __forceinline__ void lin_mma(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc,
+                                        uint32_t accumulate) {
+#define GQ_MMA(kind)                                                                                                   \
+    asm volatile(                                                                                                      \
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 b0, b1, b2, b3;\n\t"                                                      \
+        "mov.b64 b0, {%5, %10};\n\tmov.b64 b1, {%6, %10};\n\tmov.b64 b2, {%7, %10};\n\tmov.b64 b3, {%8, %10};\n\t"     \
+        "setp.ne.b32 p, %9, 0;\n\t"                                                                                    \
+        "elect.sync _|e, 0xffffffff;\n\t"                                                                              \
+        "@e tcgen05.mma." kind ".kind::f16 [%0], [%1], b0, %11, p;\n\t"                                                \
+        "@e tcgen05.mma." kind ".kind::f16 [%0], [%2], b1, %11, 1;\n\t"                                                \
+        "@e tcgen05.mma." kind ".kind::f16 [%0], [%3], b2, %11, 1;\n\t"                                                \
+        "@e tcgen05.mma." kind ".kind::f16 [%0], [%4], b3, %11, 1;\n\t"                                                \
+        "}\n" ::"r"(d_tmem),                                                                                           \
+        "r"(a_tmem), "r"(a_tmem + 8u), "r"(a_tmem + 16u), "r"(a_tmem + 24u), "r"(b_low), "r"(b_low + 2u),              \
+        "r"(b_low + 4u), "r"(b_low + 6u), "r"(accumulate), "r"((uint32_t)(g_smem_desc(0u) >> 32)), "r"(idesc)          \
+        : "memory")
+    if constexpr (CTAS == 2) GQ_MMA("cta_group::2");
+    else GQ_MMA("cta_group::1");
+#undef GQ_MMA
+}
+// A value that every lane holds, for the compiler to know it.
+__device__ __forceinline__ uint32_t lin_uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+
 // Four consecutive rows of a column from the S blocks' sums at shared address
 // `at`, added in rank order: all 4 S loads are on their way before the first
 // addition.
@@ -578,22 +609,21 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
             if (!g_wait_warp(full(q % D), (uint32_t)((q / D) & 1))) ok = false;
     } else if (warp == 1) {
         int s = 0, t = 0;
-        uint32_t ph = 0u, tph = 0u;
+        uint32_t tph = 0u;
+        const uint32_t acc = lin_uniform(tmem), b_low = lin_desc_low(base);
         for (int i = 0; i < stages; ++i) {
-            if (!g_wait_warp(full(s), ph) || !g_wait_warp(wready(t), tph)) {
+            // the warps that announce the codes have waited for the stage's copies, X among them
+            if (!g_wait_warp(wready(t), tph)) {
                 ok = false;
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const int n = min(2, kb1 - kb0 - 2 * i);
-            for (int j = 0; j < n; ++j)
-                g_mma_stage_ts(tmem, tmem + S::acc_cols + 64u * t + 32u * j, x_tile(s, j), P.idesc, i | j ? 1u : 0u);
+            const uint32_t a = acc + S::acc_cols + 64u * t, b = b_low + (uint32_t)s * (S::stage >> 4);
+            lin_mma<1>(acc, a, b, P.idesc, i ? 1u : 0u);
+            if (2 * i + 1 < kb1 - kb0) lin_mma<1>(acc, a + 32u, b + (S::x_block >> 4), P.idesc, 1u);
             g_commit(empty(s));
             g_commit(tfree(t));
-            if (++s == D) {
-                s = 0;
-                ph ^= 1u;
-            }
+            if (++s == D) s = 0;
             if (++t == (int)S::slots) {
                 t = 0;
                 tph ^= 1u;
@@ -741,24 +771,6 @@ __device__ __forceinline__ void lin_commit_both(uint32_t bar) {
         : "memory");
 }
 
-// The 4 MMAs (K = 16 each) of one column block, as g_mma_stage_ts, over both blocks.
-__device__ __forceinline__ void lin_mma_pair(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_addr, uint32_t idesc,
-                                             uint32_t accumulate) {
-    const uint64_t b0 = g_smem_desc(b_addr);
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %9, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %5, %10, p;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%2], %6, %10, 1;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%3], %7, %10, 1;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%4], %8, %10, 1;\n\t"
-        "}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(a_tmem + 8u), "r"(a_tmem + 16u), "r"(a_tmem + 24u), "l"(b0), "l"(b0 + 2u), "l"(b0 + 4u),
-        "l"(b0 + 6u), "r"(accumulate), "r"(idesc)
-        : "memory");
-}
-
 template <int QB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinParams P) {
@@ -851,27 +863,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 ok = false;
     } else if (warp == 1) {
         int s = 0, t = 0, done = 0;
-        uint32_t ph = 0u, tph = 0u;
+        uint32_t tph = 0u;
+        const uint32_t acc = lin_uniform(tmem), b_low = lin_desc_low(base);
         for (int q = pair; q < units && ok; q += pairs, ++done) {
             const LinUnit u = lin_find<kPairNT>(P, q / rtps);
             if (rank == 0) {
                 const uint32_t idesc = gemm_idesc(2 * kLinRows, (uint32_t)lin_cols(u));
                 if (done > 0 && !g_wait_warp(acc_empty, (uint32_t)(done - 1) & 1u)) ok = false;
                 for (int i = 0; i < stages && ok; ++i) {
-                    if (!g_wait_warp(full(s), ph) || !g_wait_warp(wready(t), tph)) {
+                    if (!g_wait_warp(wready(t), tph)) {    // (and with it for both blocks' copies, as in linear_kernel)
                         ok = false;
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const int n = min(2, P.kbs - 2 * i);
-                    for (int j = 0; j < n; ++j)
-                        lin_mma_pair(tmem, tmem + kPairNT + 64u * t + 32u * j, x_tile(s, j), idesc, i | j ? 1u : 0u);
+                    const uint32_t a = acc + kPairNT + 64u * t, b = b_low + (uint32_t)s * (S::stage >> 4);
+                    lin_mma<2>(acc, a, b, idesc, i ? 1u : 0u);
+                    if (2 * i + 1 < P.kbs) lin_mma<2>(acc, a + 32u, b + (S::x_block >> 4), idesc, 1u);
                     lin_commit_both(empty(s));
                     lin_commit_both(tfree(t));
-                    if (++s == D) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                    if (++s == D) s = 0;
                     if (++t == kPairSlots) {
                         t = 0;
                         tph ^= 1u;
