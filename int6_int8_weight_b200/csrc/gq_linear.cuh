@@ -120,49 +120,101 @@ struct LinEpi {
     int32_t bias_bf16, residual_bf16, y_bf16, act;
 };
 
-// 1 / (1 + 2^a), from the special function unit: 0 and 1 where 2^a over- or
-// underflows.
-__device__ __forceinline__ float lin_sigmoid2(float a) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return r;
+// Two values in a register pair: sums and products of both in one issue.
+struct LinF2 {
+    uint64_t r;
+    __device__ __forceinline__ LinF2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit LinF2(float a) : LinF2(a, a) {}
+    __device__ __forceinline__ void out(float& a, float& b) const {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+    }
+};
+__device__ __forceinline__ LinF2 lin_fma(LinF2 a, LinF2 b, LinF2 c) {
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(a.r) : "l"(a.r), "l"(b.r), "l"(c.r));
+    return a;
+}
+__device__ __forceinline__ LinF2 operator*(LinF2 a, LinF2 b) {
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a.r) : "l"(a.r), "l"(b.r));
+    return a;
+}
+__device__ __forceinline__ LinF2 operator+(LinF2 a, LinF2 b) {
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(a.r) : "l"(a.r), "l"(b.r));
+    return a;
+}
+
+// From the special function unit: 2^a and 1 / a.
+__device__ __forceinline__ float lin_exp2(float a) {
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    return a;
+}
+__device__ __forceinline__ float lin_rcp(float a) {
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    return a;
+}
+__device__ __forceinline__ float lin_relu(float a) {       // NaN stays NaN
+    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(a));
+    return a;
+}
+
+// 1 / (1 + 2^a): 0 and 1 where 2^a over- or underflows.
+__device__ __forceinline__ LinF2 lin_sigmoid2(LinF2 a) {
+    float x, y;
+    a.out(x, y);
+    (LinF2(lin_exp2(x), lin_exp2(y)) + LinF2(1.0f)).out(x, y);
+    return LinF2(lin_rcp(x), lin_rcp(y));
 }
 
 // The normal distribution function: 1 - Phi(|x|) = t (b1 + t (b2 + .. + t b5)) e^(-x^2 / 2), t = 1 / (1 + q |x|), the
 // approximation of Hastings (Abramowitz and Stegun 7.1.26, with half its coefficients), absolute error below 1e-7.
-__device__ __forceinline__ float lin_phi(float x) {
-    float t, e;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(__fmaf_rn(0.23164189f, fabsf(x), 1.0f)));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * x * -0.72134752f));
-    float p = __fmaf_rn(t, 0.5307027145f, -0.7265760135f);
-    p = __fmaf_rn(t, p, 0.7107068705f);
-    p = __fmaf_rn(t, p, -0.142248368f);
-    p = __fmaf_rn(t, p, 0.127414796f);
-    p = p * t * e;
-    return x < 0.0f ? p : 1.0f - p;
+__device__ __forceinline__ LinF2 lin_phi(float x, float y) {
+    const LinF2 z(x, y), t(lin_rcp(__fmaf_rn(0.23164189f, fabsf(x), 1.0f)), lin_rcp(__fmaf_rn(0.23164189f, fabsf(y), 1.0f)));
+    float ex, ey, px, py, ux, uy;
+    (z * z * LinF2(-0.72134752f)).out(ex, ey);
+    LinF2 p = lin_fma(t, LinF2(0.5307027145f), LinF2(-0.7265760135f));
+    p = lin_fma(t, p, LinF2(0.7107068705f));
+    p = lin_fma(t, p, LinF2(-0.142248368f));
+    p = lin_fma(t, p, LinF2(0.127414796f));
+    p = p * t * LinF2(lin_exp2(ex), lin_exp2(ey));
+    p.out(px, py);
+    lin_fma(p, LinF2(-1.0f), LinF2(1.0f)).out(ux, uy);
+    return LinF2(x < 0.0f ? px : ux, y < 0.0f ? py : uy);
 }
 
-// N values through the activation, in place.  silu and the gelus
-// take the exponential and the quotient from the special function unit: a few
-// units in the last place of a factor at most 1.  NaN stays NaN.
+// N (even) values through the activation, in place, two at a time.  silu and the
+// gelus take the exponential and the quotient from the special function unit: a
+// few units in the last place of a factor at most 1.  NaN stays NaN.
 template <int N>
 __device__ __forceinline__ void lin_act(float (&z)[N], int act) {
     // one test of `act` for all of them, and a loop of its own for each
     auto each = [&](auto f) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = f(z[i]);
+        for (int i = 0; i < N; i += 2) f(z[i], z[i + 1]).out(z[i], z[i + 1]);
     };
     switch (act) {
-        case GQ_ACT_RELU: each([](float x) { return x < 0.0f ? 0.0f : x; }); break;
-        case GQ_ACT_RELU2: each([](float x) { x = x < 0.0f ? 0.0f : x; return x * x; }); break;
-        case GQ_ACT_LEAKY_RELU2: each([](float x) { x = x < 0.0f ? 0.5f * x : x; return x * x; }); break;
-        case GQ_ACT_SILU: each([](float x) { return x * lin_sigmoid2(-1.4426950408889634f * x); }); break;
-        case GQ_ACT_GELU: each([](float x) { return x * lin_phi(x); }); break;
+        case GQ_ACT_RELU: each([](float x, float y) { return LinF2(lin_relu(x), lin_relu(y)); }); break;
+        case GQ_ACT_RELU2:
+            each([](float x, float y) {
+                const LinF2 r(lin_relu(x), lin_relu(y));
+                return r * r;
+            });
+            break;
+        case GQ_ACT_LEAKY_RELU2:
+            each([](float x, float y) {
+                float hx, hy;
+                (LinF2(x, y) * LinF2(0.5f)).out(hx, hy);
+                const LinF2 r(x < 0.0f ? hx : x, y < 0.0f ? hy : y);
+                return r * r;
+            });
+            break;
+        case GQ_ACT_SILU:
+            each([](float x, float y) { return LinF2(x, y) * lin_sigmoid2(LinF2(x, y) * LinF2(-1.4426950408889634f)); });
+            break;
+        case GQ_ACT_GELU: each([](float x, float y) { return LinF2(x, y) * lin_phi(x, y); }); break;
         case GQ_ACT_GELU_TANH:
             // tanh(w) + 1 = 2 sigmoid(2 w), 2 w = 2 sqrt(2 / pi) (x + 0.044715 x^3), here times -log2(e)
-            each([](float x) {
-                return x * lin_sigmoid2(x * __fmaf_rn(x * x, -0.10294324f, -2.3022082f));
+            each([](float x, float y) {
+                const LinF2 z(x, y);
+                return z * lin_sigmoid2(z * lin_fma(z * z, LinF2(-0.10294324f), LinF2(-2.3022082f)));
             });
             break;
         default: break;
@@ -194,12 +246,15 @@ __device__ __forceinline__ void lin_rows_out(const LinEpi& E, float (&v)[N], int
         }
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __fmaf_rn(v[i], s, b);   // (b is 0 without a bias)
+    for (int i = 0; i < N; i += 2)                         // (b is 0 without a bias)
+        lin_fma(LinF2(v[i], v[i + 1]), LinF2(s), LinF2(b)).out(v[i], v[i + 1]);
     lin_act(v, E.act);
     if constexpr (RES) {
         const int shift = E.residual_bf16 ? 16 : 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __uint_as_float(r[i] << shift);
+        for (int i = 0; i < N; i += 2)
+            (LinF2(v[i], v[i + 1]) + LinF2(__uint_as_float(r[i] << shift), __uint_as_float(r[i + 1] << shift)))
+                .out(v[i], v[i + 1]);
     }
     if (E.y_bf16) {
         uint16_t* p = static_cast<uint16_t*>(E.y) + m * E.ldy + n;
@@ -1022,7 +1077,7 @@ __global__ void __launch_bounds__(256) linear_empty_kernel(const __grid_constant
             if (m < P.offsets[e] || m >= P.offsets[e + 1]) continue;
         }
         for (int64_t n = threadIdx.x; n < P.N; n += blockDim.x) {
-            float v[1] = {0.0f};
+            float v[2] = {0.0f, 0.0f};
             lin_finish(P.epi, v, 1, 0.0f, P.epi.bias ? lin_elem(P.epi.bias, e * P.N + n, P.epi.bias_bf16) : 0.0f, m, n);
         }
     }
