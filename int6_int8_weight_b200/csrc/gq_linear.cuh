@@ -334,6 +334,23 @@ __device__ __forceinline__ void lin_tmem_drain(uint32_t taddr, float (&v)[16][4]
 #undef GQ_OUT4
 }
 
+// v[a ..] = v[b ..], 16 values, as moves that stay where they are written: from
+// assignments the compiler makes copies of the whole array on every way through
+// the pair kernel's loop (8192 rows over 32 experts: 153 us for 146, 20 moves for
+// each element of Y).
+__device__ __forceinline__ void lin_move16(float (&v)[16][4], int a, int b) {
+#define GQ_OUT4(j) "=f"(v[a + j][0]), "=f"(v[a + j][1]), "=f"(v[a + j][2]), "=f"(v[a + j][3])
+#define GQ_IN4(j) "f"(v[b + j][0]), "f"(v[b + j][1]), "f"(v[b + j][2]), "f"(v[b + j][3])
+    asm volatile("mov.b32 %0, %16;\n\tmov.b32 %1, %17;\n\tmov.b32 %2, %18;\n\tmov.b32 %3, %19;\n\t"
+                 "mov.b32 %4, %20;\n\tmov.b32 %5, %21;\n\tmov.b32 %6, %22;\n\tmov.b32 %7, %23;\n\t"
+                 "mov.b32 %8, %24;\n\tmov.b32 %9, %25;\n\tmov.b32 %10, %26;\n\tmov.b32 %11, %27;\n\t"
+                 "mov.b32 %12, %28;\n\tmov.b32 %13, %29;\n\tmov.b32 %14, %30;\n\tmov.b32 %15, %31;"
+                 : GQ_OUT4(0), GQ_OUT4(1), GQ_OUT4(2), GQ_OUT4(3)
+                 : GQ_IN4(0), GQ_IN4(1), GQ_IN4(2), GQ_IN4(3));
+#undef GQ_OUT4
+#undef GQ_IN4
+}
+
 // The binary32 at shared address `addr` of block `rank` of the cluster.
 __device__ __forceinline__ float lin_ld_peer(uint32_t addr, uint32_t rank) {
     float f;
@@ -989,10 +1006,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
                 }
                 c += 64;
-#pragma unroll
-                for (int j = 0; j < 12; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[j][i] = v[j + 4][i];
+                lin_move16(v, 0, 4);
+                lin_move16(v, 4, 8);
+                lin_move16(v, 8, 12);
                 __syncwarp();
                 continue;
             }
