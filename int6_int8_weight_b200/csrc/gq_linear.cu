@@ -83,16 +83,18 @@ gq_status launch(LinParams& P, const void* d_x, int64_t K, int64_t ldx, cudaStre
     return launch_next(linear_kernel<QB, NT>, P, units * split, S::threads, smem, split, stream);
 }
 
-// Whether the pair kernel is the faster one: 24 column blocks at least, so that a unit's hand-over counts for little;
-// enough rows that a converted code serves more tokens than the 128 of the other kernel's tiles, or nearly; and
-// units that fill the pairs' rounds to three fifths.  Measured, us, one block a tile against pairs: N = K = 8192: M 384
-// 68.1 / 48.3, M 256 41.9 / 50.8; N 8192, K 2048: M 384 23.7 / 21.2, M 2048 80.8 / 70.3; N 1536, K 512: M 1024 17.2 /
-// 15.8, M 2048 12.3 / 16.1; 32 experts of 4096 x 2048: 160 rows each 142 / 127, 512 rows 330 / 283.
+// Whether the pair kernel is the faster one: enough rows that a converted code serves more tokens than the 128 of the
+// other kernel's tiles, or nearly (an average of 64 for experts, whose counts differ); units that fill the pairs' rounds
+// to three fifths; and 24 column blocks, or more than one round, so that the first unit's way through the pipeline counts
+// for little.  Measured, us, pairs against one block a tile: N = K = 8192: M 256 45.3 / 37.6, M 320 37.6 / 63.3; N 16384, K
+// 8192: M 64 35.8 / 29.3, M 96 37.0 / 39.4; N 8192, K 2048: M 256 18.4 / 16.1, M 512 19.4 / 20.8; N 4096, K 1024: M 1024
+// 14.1 / 13.6, M 2048 19.9 / 24.4; N 1536, K 512: M 2048 11.6 / 9.6, M 8192 20.8 / 24.6; 32 experts of 4096 x 2048: 48 rows
+// each 69.8 / 69.4, 64 rows 71.0 / 79.0, 160 rows 98.7 / 132.2.
 bool pair_pays(const LinParams& P) {
     const int64_t rows = (P.M + P.E - 1) / P.E, pairs = std::max(1, sm_count() / 2);
     const int64_t units = (P.rts + 1) / 2 * (int64_t)P.E * ((rows + kPairNT - 1) / kPairNT);
     const int64_t rounds = (units + pairs - 1) / pairs;
-    return P.kbs >= 24 && rows >= 96 && 5 * units >= 3 * rounds * pairs;
+    return rows >= (P.E > 1 ? 64 : 96) && 5 * units >= 3 * rounds * pairs && (P.kbs >= 24 || rounds > 1);
 }
 
 // The kernel of 256 x 256 tiles over pairs of SMs.

@@ -205,6 +205,23 @@ def test_many_rows(gq, M, N, K, qbits, act, bias, residual, out):
     _run(gq, M, N, K, qbits, act, bias, residual, out)
 
 
+@pytest.mark.parametrize("qbits", [6, 8])
+@pytest.mark.parametrize("M,N,K", [
+    (2050, 4100, 8), (2300, 4096, 64), (2048, 4100, 72), (3000, 3000, 200), (2050, 4000, 320), (4100, 2050, 528),
+])
+def test_many_rows_of_few_columns(gq, M, N, K, qbits):
+    """Over pairs of SMs with fewer stages to a unit than there are slots for them: a unit's sums are drained while the
+    next units' stages are under way."""
+    _run(gq, M, N, K, qbits, "silu", "f32", "bf16")
+
+
+@pytest.mark.parametrize("qbits", [6, 8])
+@pytest.mark.parametrize("K", [40, 136, 264])
+def test_grouped_many_rows_of_few_columns(gq, K, qbits):
+    _grouped(gq, [70, 0, 300, 5, 64, 200, 31, 90, 128, 1, 255, 40, 77, 33, 96, 120], 2500, K, qbits, "gelu_tanh", "f32",
+             "f32", torch.bfloat16, first=1, behind=20)
+
+
 def test_more_rows_than_one_wave(gq):
     """Enough tiles that every block takes several."""
     _run(gq, 3000, 4096, 128, 6, "silu", "bf16", "bf16")
