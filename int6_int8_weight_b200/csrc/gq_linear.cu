@@ -83,18 +83,22 @@ gq_status launch(LinParams& P, const void* d_x, int64_t K, int64_t ldx, cudaStre
     return launch_next(linear_kernel<QB, NT>, P, units * split, S::threads, smem, split, stream);
 }
 
-// Whether the pair kernel is the faster one: enough rows that a converted code serves more tokens than the 128 of the
-// other kernel's tiles, or nearly (an average of 64 for experts, whose counts differ); units that fill the pairs' rounds
-// to three fifths; and 24 column blocks, or more than one round, so that the first unit's way through the pipeline counts
-// for little.  Measured, us, pairs against one block a tile: N = K = 8192: M 256 45.3 / 37.6, M 320 37.6 / 63.3; N 16384, K
-// 8192: M 64 35.8 / 29.3, M 96 37.0 / 39.4; N 8192, K 2048: M 256 18.4 / 16.1, M 512 19.4 / 20.8; N 4096, K 1024: M 1024
-// 14.1 / 13.6, M 2048 19.9 / 24.4; N 1536, K 512: M 2048 11.6 / 9.6, M 8192 20.8 / 24.6; 32 experts of 4096 x 2048: 48 rows
-// each 69.8 / 69.4, 64 rows 71.0 / 79.0, 160 rows 98.7 / 132.2.
+// Whether the pair kernel is the faster one.  Three conditions, measured in us, pairs against one block a tile:
+//  - Units that fill the pairs' rounds to three fifths: N = K = 8192: M 256 (fill 0.43) 45.3 / 37.6, M 320 (0.86) 37.6 / 63.3.
+//  - 24 column blocks in all for a pair, so that its first unit's way through the pipeline counts for little: N 4096, K
+//    1024: M 1024 (16) 14.1 / 13.6, M 2048 (32) 19.9 / 24.4; N 24576, K 256, M 256 (8) 14.3 / 11.6; 16 experts of 1584 x
+//    528, 256 rows each (18) 20.8 / 18.9; N 4096, K 200, M 8192 (28) 35.9 / 45.2.
+//  - Enough rows that a converted code serves more tokens than in the other kernel's tiles of up to 128, or nearly: N
+//    32768, K 1024: M 128 16.0 / 13.5, M 192 17.7 / 23.2; with long K from 96 rows on, N 16384, K 8192: M 64 35.8 / 29.3, M
+//    96 37.0 / 39.4, K 2048: M 128 14.9 / 16.3 (N 32768, K 1536: 19.8 / 17.4); experts, whose counts differ, from 96 rows on average, 2048 x 1024: 64 rows 18.3 / 16.9, 96 rows
+//    17.6 / 21.1, and from 64 where there is much of it, 64 experts of 4096 x 2048: 48 rows 145.8 / 142.1, 64 rows
+//    141.1 / 165.5.
 bool pair_pays(const LinParams& P) {
     const int64_t rows = (P.M + P.E - 1) / P.E, pairs = std::max(1, sm_count() / 2);
     const int64_t units = (P.rts + 1) / 2 * (int64_t)P.E * ((rows + kPairNT - 1) / kPairNT);
     const int64_t rounds = (units + pairs - 1) / pairs;
-    return rows >= (P.E > 1 ? 64 : 96) && 5 * units >= 3 * rounds * pairs && (P.kbs >= 24 || rounds > 1);
+    const int least = P.E == 1 ? (P.kbs < 32 ? 129 : 96) : (rounds >= 4 && P.kbs >= 16 ? 64 : 96);
+    return rows >= least && 5 * units >= 3 * rounds * pairs && rounds * P.kbs >= 24;
 }
 
 // The kernel of 256 x 256 tiles over pairs of SMs.
