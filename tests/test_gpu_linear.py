@@ -200,6 +200,7 @@ def test_epilogue(gq, M, act, bias, residual, out):
     (500, 5700, 1544, "none", "none", "none", torch.float32), (257, 8191, 1601, "silu", "bf16", "bf16", torch.bfloat16),
     (1100, 8192, 1536, "gelu", "f32", "f32", torch.bfloat16), (300, 8200, 2048, "gelu_tanh", "f32", "bf16", torch.float32),
     (97, 12000, 1600, "relu2", "none", "f32", torch.float32), (2500, 2050, 1664, "leaky_relu2", "bf16", "bf16", torch.bfloat16),
+    (101, 12000, 2072, "relu", "f32", "f32", torch.bfloat16),
 ])
 def test_many_rows(gq, M, N, K, qbits, act, bias, residual, out):
     _run(gq, M, N, K, qbits, act, bias, residual, out)
