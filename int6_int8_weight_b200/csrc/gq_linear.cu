@@ -141,6 +141,9 @@ gq_status linear(const void* d_x, int64_t M, int64_t K, int64_t ldx, const int32
     if (ldx > INT64_MAX / 16 / (M + 1) || ldy > INT64_MAX / 16 / (M + 1) ||
         (e.residual && e.ldr > INT64_MAX / 16 / (M + 1)))
         return GQ_ERR_INVALID_ARG;
+    // a residual that is Y itself is read and written by the same thread, which wants the same elements
+    if (e.residual && e.residual == d_y && (e.residual_dtype != e.y_dtype || (M > 1 && e.ldr != ldy)))
+        return GQ_ERR_INVALID_ARG;
     if (d_status && !aligned(d_status, 4)) return GQ_ERR_MISALIGNED;
     const bool empty = M == 0 || N == 0 || E == 0;
     if (!empty) {

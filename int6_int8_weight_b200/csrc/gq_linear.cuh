@@ -506,23 +506,58 @@ __device__ __forceinline__ int lin_total(const LinParams& P) {
 // The MMAs' N for a unit of the pair kernel: its rows in steps of 32.
 __device__ __forceinline__ int lin_cols(const LinUnit& u) { return u.m1 - u.m0 + 31 & ~31; }
 
-// Unit `tt` of the token tiles (expert-major) found by one warp: every lane
-// scans its share of the experts' tile counts.  m0 = m1 past the last.
+// The inclusive prefix sum of the lanes' tile counts, held at 2^30 (only offsets that are out of order could carry it
+// past the rows' number).
+__device__ __forceinline__ int lin_prefix(int n) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, n, d);
+        if (lane >= d) n = (int)min((unsigned)n + (unsigned)o, 1u << 30);
+    }
+    return n;
+}
+
+// Unit `tt` of the token tiles (expert-major) found by one warp: every lane counts
+// the tiles of its share of the experts, all its loads in flight, then the lanes look
+// at one expert each of the share that holds the unit (8 rows, N 512, K 2048, 512
+// experts: 6.7 us, and 10.6 with 32 experts after the other).  m0 = m1 past the last.
 template <int NT>
 __device__ __forceinline__ LinUnit lin_find(const LinParams& P, int tt) {
     LinUnit u{0, 0, 0, 0, 0};
-    const int M = (int)P.M;
+    const int M = (int)P.M, E = (int)P.E;
     if (!P.offsets) {
         lin_cut<NT>(u, 0, M, tt);
         return u;
     }
     const int lane = threadIdx.x & 31;
-    int before = 0;                                        // tiles of the experts before this round's
-    for (int e0 = 0; e0 < (int)P.E; e0 += 32) {
+    int first = 0, last = E, before = 0;                   // experts to look at, tiles of those before them
+    if (E > 32) {
+        const int share = (E + 31) >> 5, a = min(lane * share, E), b = min(a + share, E);
+        int sum = 0, p = __ldg(P.offsets + a);
+        bool ok = true;
+#pragma unroll 8
+        for (int e = a; e < b; ++e) {
+            const int q = __ldg(P.offsets + e + 1);
+            const bool in = p >= 0 && q >= p && q <= M;
+            ok = ok && in;
+            sum = (int)min((unsigned)sum + (in ? ((unsigned)(q - p) + NT - 1u) / NT : 0u), 1u << 30);
+            p = q;
+        }
+        if (!__all_sync(0xffffffffu, ok)) u.bad = 1;
+        const int at = lin_prefix(sum);
+        const uint32_t who = __ballot_sync(0xffffffffu, sum > 0 && tt < at && tt >= at - sum);
+        if (!who) return u;
+        const int l = __ffs(who) - 1;
+        before = __shfl_sync(0xffffffffu, at - sum, l);
+        first = l * share;
+        last = min(first + share, E);
+    }
+    for (int e0 = first; e0 < last; e0 += 32) {
         const int e = e0 + lane;
         int a = 0, b = 0;
         bool ok = true;
-        if (e < (int)P.E) {
+        if (e < last) {
             const int p = __ldg(P.offsets + e), q = __ldg(P.offsets + e + 1);
             ok = p >= 0 && q >= p && q <= M;
             a = ok ? p : 0;
@@ -530,21 +565,14 @@ __device__ __forceinline__ LinUnit lin_find(const LinParams& P, int tt) {
         }
         if (!__all_sync(0xffffffffu, ok)) u.bad = 1;
         const int n = (int)(((unsigned)(b - a) + NT - 1u) / NT);
-        // inclusive prefix sum, held at 2^30 (only offsets that are out of order could carry it past the rows' number)
-        int sum = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum = (int)min((unsigned)sum + (unsigned)o, 1u << 30);
-        }
-        const int at = (int)min((unsigned)before + (unsigned)sum, 1u << 30);   // tiles up to and with this expert's
+        const int at = (int)min((unsigned)before + (unsigned)lin_prefix(n), 1u << 30);   // tiles up to and with this expert's
         const uint32_t who = __ballot_sync(0xffffffffu, n > 0 && tt < at && tt >= at - n);
-        if (who && u.m1 == 0) {
+        if (who) {
             const int l = __ffs(who) - 1;
             u.e = e0 + l;
             lin_cut<NT>(u, __shfl_sync(0xffffffffu, a, l), __shfl_sync(0xffffffffu, b, l),
                         __shfl_sync(0xffffffffu, tt - (at - n), l));
-            if (blockIdx.x != 0) return u;                 // block 0 reads on: every offset is checked
+            return u;
         }
         before = __shfl_sync(0xffffffffu, at, 31);
     }

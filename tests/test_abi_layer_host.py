@@ -82,6 +82,8 @@ def test_product_errors(gq, grouped):
                       (dict(bias=T + 2), 3), (dict(bias=T + 1, bias_dtype=1), 3), (dict(residual=T + 2, ldr=8), 3)):
         assert call(epi) == code, epi
     assert call(dict(y_dtype=0), y=Y + 2) == 3
+    # a residual that is Y itself has Y's type and pitch
+    assert call(dict(residual=Y, ldr=8, residual_dtype=0)) == 1 and call(dict(residual=Y, ldr=16, residual_dtype=1)) == 1
     for kw in (dict(M=0, x=None, y=None), dict(N=0, t=None, y=None)):
         assert call(**kw) == 0
     if grouped:

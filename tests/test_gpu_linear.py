@@ -466,6 +466,32 @@ def test_grouped_bad_offsets_are_reported(gq):
         gq.gemm_grouped(_x(rng, 5, 64), off, gq.tile_weight(W.packed, 64, 6), W.scale, 6, check_status=True)
 
 
+@pytest.mark.parametrize("E,active,rows,N,K", [
+    (33, 33, 3, 130, 64), (100, 7, 40, 200, 72), (300, 300, 2, 130, 40), (1100, 25, 30, 70, 64), (2500, 3, 1, 64, 24),
+    (40, 40, 120, 2500, 1600), (700, 90, 90, 1000, 24),
+])
+def test_grouped_many_experts(gq, E, active, rows, N, K):
+    """More experts than lanes of a warp, most of them without a row."""
+    counts = np.zeros(E, np.int64)
+    rng = np.random.default_rng(E)
+    counts[rng.permutation(E)[:active]] = rng.integers(1, 2 * rows, active)
+    counts[E - 1] = max(counts[E - 1], 1)
+    _grouped(gq, counts.tolist(), N, K, 6, "silu", "f32", "bf16", torch.bfloat16, first=2, behind=3)
+
+
+def test_grouped_bad_offsets_of_many_experts(gq):
+    rng = np.random.default_rng(13)
+    W = Weight(gq, rng, 300, 64, 64, 8)
+    x, tiles = _x(rng, 90, 64), gq.tile_weight(W.packed, 64, 8)
+    for at, value in ((0, -1), (1, 91), (150, 3), (299, 91), (300, 60), (300, 1 << 30)):
+        off = np.minimum(np.arange(301), 90).astype(np.int32)
+        off[at] = value
+        pad = torch.full((92, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        with pytest.raises(gq.GQError, match="0x8"):
+            gq.gemm_grouped(x, torch.from_numpy(off).cuda(), tiles, W.scale, 8, y=pad[1:91], check_status=True)
+        assert (pad[0] == 7).all() and (pad[91] == 7).all()
+
+
 def test_grouped_bad_offsets_overlapping(gq):
     """Expert ranges that overlap, each in order by itself: reported, and none of their tiles worked on by the pairs of
     SMs (65535 experts of the whole batch would be as many products).  With no columns too."""
