@@ -12,7 +12,7 @@ using namespace gq;
 
 static_assert(sizeof(gq_adamw_tensor) == 88 && sizeof(gq_adamw_hyper) == 72,
               "the layouts are part of the ABI (the Python binding mirrors them)");
-static_assert(sizeof(AdamParams) <= 32764, "kernel parameters end at 32764 bytes");
+static_assert(sizeof(AdamParams<kAdamDesc>) <= 32764, "kernel parameters end at 32764 bytes");
 
 gq_status check_adamw(const gq_adamw_tensor& t) {
     if (t.reserved != 0 || t.numel < 0) return GQ_ERR_INVALID_ARG;
@@ -31,46 +31,18 @@ gq_status check_adamw(const gq_adamw_tensor& t) {
     return GQ_OK;
 }
 
-}  // namespace
-
-extern "C" gq_status gq_adamw_step(const gq_adamw_tensor* t, int n, const gq_adamw_hyper* h, cudaStream_t stream) {
-    if (n < 0 || (n > 0 && !t) || !h) return GQ_ERR_INVALID_ARG;
-    if (!(h->beta1 >= 0.0 && h->beta1 < 1.0) || !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps >= 0.0) ||
-        !std::isfinite(h->eps) || !std::isfinite(h->lr) || (!h->d_step && h->step < 1))
-        return GQ_ERR_INVALID_ARG;
-    if ((h->d_step && !aligned(h->d_step, 8)) || (h->d_lr && !aligned(h->d_lr, 4)) ||
-        (h->d_grad_scale && !aligned(h->d_grad_scale, 4)))
-        return GQ_ERR_MISALIGNED;
-    for (int i = 0; i < n; ++i) {
-        const gq_status st = check_adamw(t[i]);
-        if (st != GQ_OK) return st;
-    }
-    AdamParams P;
-    const int64_t step = h->d_step ? 1 : h->step;
-    P.lr = h->lr;
-    P.beta1 = h->beta1;
-    P.beta2 = h->beta2;
-    P.bias1 = 1.0 - std::pow(h->beta1, (double)step);
-    P.b1 = (float)h->beta1;
-    P.c1 = (float)(1.0 - h->beta1);
-    P.b2 = (float)h->beta2;
-    P.c2 = (float)(1.0 - h->beta2);
-    P.eps = (float)h->eps;
-    P.one = 1.0f;
-    P.paired = P.eps <= kAdamHigh / 4.0f;
-    P.inv_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h->beta2, (double)step)));
-    P.step_size = (float)(h->lr / P.bias1);
-    P.key_step = (uint32_t)step * kAdamStepMul;
-    P.d_step = h->d_step;
-    P.d_lr = h->d_lr;
-    P.d_grad_scale = h->d_grad_scale;
-    // the tensors with 8-bit states and those with 32-bit ones, up to kAdamDesc a launch
+// The launches of a step; S holds all that does not depend on the tensors.
+template <int CAP>
+gq_status launch_adamw(const gq_adamw_tensor* t, int n, const gq_adamw_hyper* h, const AdamStep& S, cudaStream_t stream) {
+    AdamParams<CAP> P;
+    static_cast<AdamStep&>(P) = S;
+    // the tensors with 8-bit states and those with 32-bit ones, up to CAP a launch
     for (const bool s8 : {false, true}) {
         int i = 0;
         while (i < n) {
             int64_t items = 0;
             P.ndesc = 0;
-            for (; i < n && P.ndesc < kAdamDesc; ++i) {
+            for (; i < n && P.ndesc < CAP; ++i) {
                 const gq_adamw_tensor& T = t[i];
                 if (T.numel == 0 || (T.state_bits == 8) != s8) continue;
                 AdamDesc& D = P.d[P.ndesc];
@@ -97,10 +69,46 @@ extern "C" gq_status gq_adamw_step(const gq_adamw_tensor* t, int n, const gq_ada
             P.start[P.ndesc] = items;
             if (items == 0) continue;
             const unsigned blocks = (unsigned)std::min<int64_t>(items, (int64_t)sm_count() * 32);
-            if (s8) adamw_kernel<true><<<blocks, kAdamThreads, 0, stream>>>(P);
-            else adamw_kernel<false><<<blocks, kAdamThreads, 0, stream>>>(P);
+            if (s8) adamw_kernel<true, CAP><<<blocks, kAdamThreads, 0, stream>>>(P);
+            else adamw_kernel<false, CAP><<<blocks, kAdamThreads, 0, stream>>>(P);
             if (launch_status() != GQ_OK) return GQ_ERR_CUDA;
         }
     }
     return GQ_OK;
+}
+
+}  // namespace
+
+extern "C" gq_status gq_adamw_step(const gq_adamw_tensor* t, int n, const gq_adamw_hyper* h, cudaStream_t stream) {
+    if (n < 0 || (n > 0 && !t) || !h) return GQ_ERR_INVALID_ARG;
+    if (!(h->beta1 >= 0.0 && h->beta1 < 1.0) || !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(h->eps >= 0.0) ||
+        !std::isfinite(h->eps) || !std::isfinite(h->lr) || (!h->d_step && h->step < 1))
+        return GQ_ERR_INVALID_ARG;
+    if ((h->d_step && !aligned(h->d_step, 8)) || (h->d_lr && !aligned(h->d_lr, 4)) ||
+        (h->d_grad_scale && !aligned(h->d_grad_scale, 4)))
+        return GQ_ERR_MISALIGNED;
+    for (int i = 0; i < n; ++i) {
+        const gq_status st = check_adamw(t[i]);
+        if (st != GQ_OK) return st;
+    }
+    AdamStep S{};
+    const int64_t step = h->d_step ? 1 : h->step;
+    S.lr = h->lr;
+    S.beta1 = h->beta1;
+    S.beta2 = h->beta2;
+    S.bias1 = 1.0 - std::pow(h->beta1, (double)step);
+    S.b1 = (float)h->beta1;
+    S.c1 = (float)(1.0 - h->beta1);
+    S.b2 = (float)h->beta2;
+    S.c2 = (float)(1.0 - h->beta2);
+    S.eps = (float)h->eps;
+    S.one = 1.0f;
+    S.paired = S.eps <= kAdamHigh / 4.0f;
+    S.inv_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h->beta2, (double)step)));
+    S.step_size = (float)(h->lr / S.bias1);
+    S.key_step = (uint32_t)step * kAdamStepMul;
+    S.d_step = h->d_step;
+    S.d_lr = h->d_lr;
+    S.d_grad_scale = h->d_grad_scale;
+    return n <= kAdamFew ? launch_adamw<kAdamFew>(t, n, h, S, stream) : launch_adamw<kAdamDesc>(t, n, h, S, stream);
 }

@@ -22,6 +22,7 @@
 namespace gq {
 
 constexpr int kAdamDesc = 200;            // tensors a launch (the parameter block stays below 32 KB)
+constexpr int kAdamFew = 16;              // a batch of no more takes a small block: 18 KB of parameters cost the host time
 constexpr int kAdamThreads = 256;
 constexpr int kAdamItem = 8 * kAdamThreads;
 constexpr float kAdamLow = 8.673617379884035e-19f, kAdamHigh = 1.152921504606847e18f;   // 2^-60, 2^60
@@ -45,7 +46,7 @@ struct AdamDesc {
 
 constexpr int32_t kAdamPBf16 = 1, kAdamGBf16 = 2, kAdamVec = 4;
 
-struct AdamParams {
+struct AdamStep {
     int32_t ndesc;
     uint32_t key_step;    // the step's share of the hash key
     double lr, beta1, beta2;
@@ -58,8 +59,12 @@ struct AdamParams {
     const int64_t* d_step;
     const float* d_lr;
     const float* d_grad_scale;
-    int64_t start[kAdamDesc + 1];   // prefix sums of work items
-    AdamDesc d[kAdamDesc];
+};
+
+template <int CAP>
+struct AdamParams : AdamStep {
+    int64_t start[CAP + 1];         // prefix sums of work items
+    AdamDesc d[CAP];
 };
 
 constexpr uint32_t kAdamStepMul = 0x632BE5ABu, kAdamTensorMul = 0x2C1B3C6Du;
@@ -235,8 +240,8 @@ __device__ __forceinline__ void adam_store8(const uint32_t (&c)[2], void* base, 
 }
 
 // S8: the launch's tensors have 8-bit states.
-template <bool S8>
-__global__ void __launch_bounds__(kAdamThreads, S8 ? 5 : 4) adamw_kernel(const __grid_constant__ AdamParams P) {
+template <bool S8, int CAP>
+__global__ void __launch_bounds__(kAdamThreads, S8 ? 5 : 4) adamw_kernel(const __grid_constant__ AdamParams<CAP> P) {
     __shared__ float s_step[3];
     float inv_bc2 = P.inv_bc2, step_size = P.step_size;
     double lr = P.lr;

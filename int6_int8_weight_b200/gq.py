@@ -22,7 +22,7 @@ import ctypes as C
 import os
 import struct
 from dataclasses import dataclass
-from itertools import repeat
+from itertools import chain, repeat
 from operator import attrgetter
 
 import torch
@@ -555,6 +555,7 @@ def _on(index: int, stream, fn, *args) -> int:
 
 _DTYPE_CODES = {torch.float32: GQ_F32, torch.bfloat16: GQ_BF16}
 _ADAMW_TENSOR = struct.Struct("@PPPPPPPqiiiid")              # gq_adamw_tensor
+_ADAMW_HYPER = struct.Struct("@ddddqQPPP")                   # gq_adamw_hyper
 _numel, _is_contiguous, _get_device = torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.get_device
 _data_ptr, _get_dtype = torch.Tensor.data_ptr, attrgetter("dtype")
 _EPILOGUE = struct.Struct("@PPqiiii")                      # gq_epilogue
@@ -691,6 +692,17 @@ def gemm_grouped(x: torch.Tensor, offsets: torch.Tensor, tiles: torch.Tensor, sc
                   out_dtype, stream, check_status)
 
 
+def _scalar(name, value, dtype, dev) -> int:
+    """The address of a one-element device tensor, 0 for a number."""
+    if not isinstance(value, torch.Tensor):
+        return 0
+    if value.dtype != dtype or value.numel() != 1:
+        raise ValueError(f"{name} on the device is one {dtype} element")
+    if value.get_device() != dev:
+        raise ValueError("every tensor of a call lies on one device")
+    return value.data_ptr()
+
+
 def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
                weight_decay=0.01, scales=None, copies=None, grad_scale: torch.Tensor | None = None, seed: int = 0,
                stream=None) -> None:
@@ -707,34 +719,33 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     n = len(params)
     if n == 0 and not (len(grads) or len(exp_avgs) or len(exp_avg_sqs)):
         return
-    # whole lists at a time: a loop over the tensors would take longer than the step of a small model
+    # all tensors at a time: a loop over them would take longer than the step of a small model
     bits = 32 if scales is None else 8
     lists = [params, grads, exp_avgs, exp_avg_sqs]
     if bits == 8:
         lists += scales
     if len(lists) not in (4, 6) or any(len(ts) != n for ts in lists) or (copies is not None and len(copies) != n):
         raise ValueError("params, grads, states, scales and copies are lists of one length")
-    numel = list(map(_numel, params))
-    dev = params[0].get_device()
-    for ts in lists:
-        if not all(map(_is_contiguous, ts)):
-            raise ValueError("weights, gradients, states and scales are contiguous")
-        if set(map(_get_device, ts)) != {dev}:
-            raise ValueError("every tensor of a call lies on one device")
-    for ts in lists[1:4]:
-        if list(map(_numel, ts)) != numel:
-            raise ValueError("weights, gradients and states are of one size")
+    flat = list(chain.from_iterable(lists))
+    if not all(map(_is_contiguous, flat)):
+        raise ValueError("weights, gradients, states and scales are contiguous")
+    dev = flat[0].get_device()
+    if set(map(_get_device, flat)) != {dev}:
+        raise ValueError("every tensor of a call lies on one device")
+    sizes, dtypes = list(map(_numel, flat)), list(map(_get_dtype, flat))
+    numel = sizes[:n]
+    if sizes[n:4 * n] != numel * 3:
+        raise ValueError("weights, gradients and states are of one size")
     try:
-        p_codes, g_codes = ([_DTYPE_CODES[k] for k in map(_get_dtype, ts)] for ts in (params, grads))
+        codes = [_DTYPE_CODES[k] for k in dtypes[:2 * n]]
     except KeyError as e:
         raise TypeError(f"weights and gradients are float32 or bfloat16, got {e.args[0]}") from None
-    if set(map(_get_dtype, exp_avgs)) != {torch.float32 if bits == 32 else torch.int8} \
-            or set(map(_get_dtype, exp_avg_sqs)) != {torch.float32 if bits == 32 else torch.uint8}:
+    if set(dtypes[2 * n:3 * n]) != {torch.float32 if bits == 32 else torch.int8} \
+            or set(dtypes[3 * n:4 * n]) != {torch.float32 if bits == 32 else torch.uint8}:
         raise TypeError("states are fp32, or int8 / uint8 codes with scales")
-    if bits == 8:
-        blocks = [-(-k // ADAMW_BLOCK) for k in numel]
-        if any(list(map(_numel, ts)) != blocks or set(map(_get_dtype, ts)) != {torch.float32} for ts in scales):
-            raise ValueError("scales are contiguous fp32 tensors of ceil(numel / 256) elements")
+    if bits == 8 and (sizes[4 * n:] != [-(-k // ADAMW_BLOCK) for k in numel] * 2
+                      or set(dtypes[4 * n:]) != {torch.float32}):
+        raise ValueError("scales are contiguous fp32 tensors of ceil(numel / 256) elements")
     copy = repeat(0)
     if copies is not None:
         for c, k in zip(copies, numel):
@@ -745,21 +756,15 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     one = isinstance(weight_decay, (int, float))
     if not one and len(weight_decay) != n:
         raise ValueError("weight_decay is a number or one per tensor")
-    pointers = [map(_data_ptr, ts) for ts in lists] + [repeat(0)] * (6 - len(lists))
-    desc = b"".join(map(_ADAMW_TENSOR.pack, *pointers, copy, numel, p_codes, g_codes, repeat(bits), repeat(0),
+    ptr = list(map(_data_ptr, flat))
+    pointers = [ptr[i:i + n] for i in range(0, len(ptr), n)] + [repeat(0)] * (6 - len(lists))
+    desc = b"".join(map(_ADAMW_TENSOR.pack, *pointers, copy, numel, codes[:n], codes[n:], repeat(bits), repeat(0),
                         repeat(weight_decay) if one else weight_decay))
-    h = GQAdamWHyper(beta1=betas[0], beta2=betas[1], eps=eps, seed=seed & 0xFFFFFFFF)
-    for name, value, dtype in (("step", step, torch.int64), ("lr", lr, torch.float32),
-                               ("grad_scale", grad_scale, torch.float32)):
-        if isinstance(value, torch.Tensor):
-            if value.dtype != dtype or value.numel() != 1:
-                raise ValueError(f"{name} on the device is one {dtype} element")
-            if value.get_device() != dev:
-                raise ValueError("every tensor of a call lies on one device")
-            setattr(h, "d_" + name, value.data_ptr())
-        elif value is not None:
-            setattr(h, name, value)
-    _check(_on(dev, stream, LIB.gq_adamw_step, desc, n, C.byref(h)), "gq_adamw_step")
+    d_step, d_lr = _scalar("step", step, torch.int64, dev), _scalar("lr", lr, torch.float32, dev)
+    d_scale = 0 if grad_scale is None else _scalar("grad_scale", grad_scale, torch.float32, dev)
+    h = _ADAMW_HYPER.pack(0.0 if d_lr else lr, *betas, eps, 0 if d_step else step, seed & 0xFFFFFFFF, d_step, d_lr,
+                          d_scale)
+    _check(_on(dev, stream, LIB.gq_adamw_step, desc, n, GQAdamWHyper.from_buffer_copy(h)), "gq_adamw_step")
 
 
 def ste_bwd(g_out: torch.Tensor, g_w: torch.Tensor | None = None, stream=None) -> torch.Tensor:
