@@ -783,6 +783,7 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
                 } else if (n < P.N) {
                     lin_finish(P.epi, v, mv - c0, sc, bi, (int64_t)u.m0 + c0, n);
                 }
+                __syncwarp();                              // the next load wants the warp whole again
             }
         }
     }
@@ -802,6 +803,7 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
                 else lin_gather<8>(v, at);
                 lin_finish(P.epi, v, mv - c, sc, bi, (int64_t)u.m0 + c, n);
             }
+        __syncwarp();                                      // lanes past the last column skipped the loop
         lin_cluster_sync();                                // its memory is read until here
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
