@@ -553,6 +553,23 @@ def _on(index: int, stream, fn, *args) -> int:
         return fn(*args, _stream(stream))
 
 
+def _on_given(stream, index: int, y, fn, *args) -> torch.Tensor:
+    """``fn(*args)`` with ``stream`` current: the memory that it allocates is that stream's (the allocator hands it out
+    again in the order of that stream's work), and what it reads back waits for that stream.  A new result (``y`` is None)
+    is kept for the caller's own stream too, which is to use it."""
+    if index < 0:
+        raise ValueError("libgq takes CUDA tensors")
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=index)
+    if stream.device_index != index:
+        raise ValueError("the stream is one of the tensors' device")
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    if y is None:
+        out.record_stream(torch.cuda.current_stream(index))
+    return out
+
+
 _DTYPE_CODES = {torch.float32: GQ_F32, torch.bfloat16: GQ_BF16}
 _ADAMW_TENSOR = struct.Struct("@PPPPPPPqiiiid")              # gq_adamw_tensor
 _ADAMW_HYPER = struct.Struct("@ddddqQPPP")                   # gq_adamw_hyper
@@ -567,6 +584,8 @@ def tile_weight(packed: torch.Tensor, K: int, qbits: int, stream=None) -> torch.
     export or at load: ``packed`` uint8 [N, packed row bytes] (or [E, N, packed
     row bytes], one weight per expert) of K columns -> uint8 [bytes] ([E, bytes]),
     the weight argument of ``gemm_epilogue`` (``gemm_grouped``)."""
+    if stream is not None:
+        return _on_given(stream, packed.get_device(), None, tile_weight, packed, K, qbits)
     if packed.dtype != torch.uint8 or packed.dim() not in (2, 3) or not packed.is_contiguous():
         raise ValueError("packed must be a contiguous uint8 [N, row bytes] or [E, N, row bytes] tensor")
     if qbits not in (6, 8) or packed.shape[-1] != gq_packed_row_bytes(K, qbits):
@@ -575,7 +594,7 @@ def tile_weight(packed: torch.Tensor, K: int, qbits: int, stream=None) -> torch.
     E, N = (1, packed.shape[0]) if packed.dim() == 2 else packed.shape[:2]
     nbytes = LIB.gq_tile_bytes(N, K, qbits)
     tiles = torch.empty((nbytes,) if packed.dim() == 2 else (E, nbytes), dtype=torch.uint8, device=packed.device)
-    _check(_on(packed.get_device(), stream, LIB.gq_tile_weight, packed.data_ptr(), E, N, K, qbits, tiles.data_ptr()),
+    _check(_on(packed.get_device(), None, LIB.gq_tile_weight, packed.data_ptr(), E, N, K, qbits, tiles.data_ptr()),
            "gq_tile_weight")
     return tiles
 
@@ -593,6 +612,9 @@ def _rows(t, M, N):
 def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, out_dtype, stream, check_status):
     """Argument checks and the call shared by gemm_epilogue and gemm_grouped.
     (Written for few Python operations: a small layer's kernel takes less time than they do.)"""
+    if stream is not None:
+        return _on_given(stream, x.get_device(), y, _layer, where, fn, x, offsets, tiles, scale, qbits, bias, act,
+                         residual, y, out_dtype, None, check_status)
     if x.dtype is not torch.bfloat16 or x.dim() != 2:
         raise ValueError("x must be a bf16 [M, K] tensor with contiguous rows")
     M, K = x.shape
@@ -650,10 +672,10 @@ def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, o
             None if st is None else st.data_ptr())
     if offsets is not None:
         args = (*args[:4], offsets.data_ptr(), shape[0], *args[4:])
-    if stream is None and dev == torch.cuda.current_device():
+    if dev == torch.cuda.current_device():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        status = _on(dev, stream, fn, *args)
+        status = _on(dev, None, fn, *args)
     if status:
         _check(status, where)
     if check_status and (v := int(st.item())):

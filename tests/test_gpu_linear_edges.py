@@ -1,14 +1,16 @@
 """GPU parity of the layer products where a kernel's own structure has an edge: the last column tile ends inside a warp
-and the epilogue makes several trips, alone and with the K range shared by a cluster.
+and the epilogue makes several trips, alone and with the K range shared by a cluster; and the binding's edges: calls on a
+stream other than the current one.
 
 Reference, tolerances and inputs are those of test_gpu_linear.py.
 """
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_linear import _grouped, _run
+from tests.test_gpu_linear import Weight, _check, _grouped, _run, _x
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +34,67 @@ def test_last_columns_end_inside_a_warp(gq, M, N, K):
 def test_last_columns_of_experts_end_inside_a_warp(gq):
     for counts, K in (([20, 0, 32, 11], 64), ([20, 0, 32, 11], 2048), ([100, 70, 0, 120], 128), ([100, 70, 0, 120], 1536)):
         _grouped(gq, counts, 161, K, 8, "relu2", "bf16", "f32", torch.bfloat16, first=1, behind=2)
+
+
+def _busy(stream, ms=100):
+    """`stream` behind what is queued already, and busy for about `ms`."""
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(ms * 1.9e6))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_status_of_a_call_on_another_stream(gq, raw):
+    """check_status waits for the call on the stream that it runs on: a bad offset is reported, a good call is not taken
+    for a bad one by what the status word's memory held before."""
+    rng = np.random.default_rng(21)
+    W = Weight(gq, rng, 2, 130, 192, 6)
+    tiles, x = gq.tile_weight(W.packed, 192, 6), _x(rng, 20, 192)
+    good, bad = (torch.tensor(o, dtype=torch.int32, device="cuda") for o in ([0, 7, 20], [0, 7, 21]))
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    for s in (torch.cuda.current_stream(), side):              # memory that the status word may come from
+        with torch.cuda.stream(s):
+            keep = [torch.full((1,), 8, dtype=torch.int32, device="cuda") for _ in range(64)]
+    torch.cuda.synchronize()
+    del keep
+    _busy(side)
+    y = gq.gemm_grouped(x, good, tiles, W.scale, 6, stream=stream, check_status=True)
+    assert side.query()                                        # the call was waited for
+    _check(y[:7], x[:7], W.w[0], None, None, "none", raw)
+    _check(y[7:], x[7:], W.w[1], None, None, "none", raw)
+    _busy(side)
+    with pytest.raises(gq.GQError, match="0x8"):
+        gq.gemm_grouped(x, bad, tiles, W.scale, 6, stream=stream, check_status=True)
+
+
+def test_results_on_another_stream_keep_their_memory(gq):
+    """A result dropped while its call is still queued on another stream is not handed out to the current one."""
+    rng = np.random.default_rng(22)
+    W = Weight(gq, rng, 1, 200, 320, 8)
+    tiles, x = gq.tile_weight(W.packed[0], 320, 8), _x(rng, 9, 320)
+    want = gq.gemm_epilogue(x, tiles, W.scale[0], 8)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda: gq.gemm_epilogue(x, tiles, W.scale[0], 8, stream=side),
+                 lambda: gq.tile_weight(W.packed[0], 320, 8, stream=side)):
+        _busy(side)
+        out = call()
+        shape, dtype, at = out.shape, out.dtype, out.data_ptr()
+        del out
+        others = [torch.empty(shape, dtype=dtype, device="cuda") for _ in range(16)]
+        assert all(t.data_ptr() != at for t in others) and not side.query()
+        torch.cuda.synchronize()
+    _busy(side, 20)
+    y = gq.gemm_epilogue(x, gq.tile_weight(W.packed[0], 320, 8, stream=side), W.scale[0], 8, stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_stream_refusals(gq):
+    W = Weight(gq, np.random.default_rng(23), 1, 64, 64, 6)
+    x = _x(np.random.default_rng(23), 3, 64)
+    with pytest.raises(ValueError):
+        gq.gemm_epilogue(x.cpu(), W.packed[0], W.scale[0], 6, stream=torch.cuda.Stream())
+    with pytest.raises(ValueError):
+        gq.tile_weight(W.packed[0].cpu(), 64, 6, stream=torch.cuda.Stream())
