@@ -575,6 +575,7 @@ _ADAMW_TENSOR = struct.Struct("@PPPPPPPqiiiid")              # gq_adamw_tensor
 _ADAMW_HYPER = struct.Struct("@ddddqQPPP")                   # gq_adamw_hyper
 _numel, _is_contiguous, _get_device = torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.get_device
 _data_ptr, _get_dtype = torch.Tensor.data_ptr, attrgetter("dtype")
+_written = torch.autograd.graph.increment_version          # of tensors that a kernel wrote in place
 _EPILOGUE = struct.Struct("@PPqiiii")                      # gq_epilogue
 _EPILOGUE_NONE = {(a, y): _EPILOGUE.pack(0, 0, 0, 0, 0, a, y) for a in ACTS.values() for y in (GQ_F32, GQ_BF16)}
 
@@ -787,6 +788,11 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     h = _ADAMW_HYPER.pack(0.0 if d_lr else lr, *betas, eps, 0 if d_step else step, seed & 0xFFFFFFFF, d_step, d_lr,
                           d_scale)
     _check(_on(dev, stream, LIB.gq_adamw_step, desc, n, GQAdamWHyper.from_buffer_copy(h)), "gq_adamw_step")
+    # written behind autograd's back: a graph that saved one of them is not to be run backwards any more
+    _written(flat[:n])
+    _written(flat[2 * n:])
+    if copies is not None:
+        _written([c for c in copies if c is not None])
 
 
 def ste_bwd(g_out: torch.Tensor, g_w: torch.Tensor | None = None, stream=None) -> torch.Tensor:

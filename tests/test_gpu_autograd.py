@@ -1,0 +1,41 @@
+"""The layer products and the AdamW step beside autograd: what they write in place is known to it."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from int6_int8_weight_b200 import gq as mod
+    return mod
+
+
+def _state(bits, n):
+    if bits == 32:
+        return [torch.zeros(n, device="cuda")], [torch.zeros(n, device="cuda")], None
+    return ([torch.zeros(n, dtype=torch.int8, device="cuda")], [torch.zeros(n, dtype=torch.uint8, device="cuda")],
+            tuple([torch.zeros(-(-n // 256), device="cuda")] for _ in range(2)))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_graph_kept_over_a_step_is_refused(gq, bits):
+    """The backward pass of a graph that saved a weight before the step raises, as with torch's optimizers."""
+    w = torch.randn(600, device="cuda", requires_grad=True)
+    x = torch.randn(600, device="cuda", requires_grad=True)
+    loss = (w * x).sum()                                       # saves w for x's gradient
+    m, v, scales = _state(bits, 600)
+    copy = torch.zeros(600, dtype=torch.bfloat16, device="cuda")
+    written = [w, m[0], v[0], copy] + ([] if scales is None else [scales[0][0], scales[1][0]])
+    before, grad = [t._version for t in written], torch.ones(600, device="cuda")
+    with torch.no_grad():
+        gq.adamw_step([w], [grad], m, v, step=1, lr=1e-3, scales=scales, copies=[copy])
+    assert all(t._version > b for t, b in zip(written, before)) and grad._version == 0
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    (w * x).sum().backward()                                   # a graph made after the step is sound
+    assert torch.equal(x.grad, w.detach())
