@@ -637,6 +637,7 @@ def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, o
         raise ValueError(f"act is one of {', '.join(ACTS)}")
     dev = x.get_device()
     same = tiles.get_device() == dev == scale.get_device()
+    given = y
     if y is None:
         y_code = 1 if out_dtype is None else _DTYPE_CODES.get(out_dtype)
         if y_code is not None and same and dev >= 0:
@@ -679,6 +680,8 @@ def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, o
         status = _on(dev, None, fn, *args)
     if status:
         _check(status, where)
+    if given is not None:
+        _written(y)
     if check_status and (v := int(st.item())):
         raise GQError(0, where, f"device status {v:#x}")
     return y

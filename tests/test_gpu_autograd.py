@@ -39,3 +39,16 @@ def test_a_graph_kept_over_a_step_is_refused(gq, bits):
         loss.backward()
     (w * x).sum().backward()                                   # a graph made after the step is sound
     assert torch.equal(x.grad, w.detach())
+
+
+def test_a_result_in_place_of_a_saved_tensor_is_refused(gq):
+    """y that a graph has saved, written over."""
+    w = torch.randn(40, 64, device="cuda")
+    (o,) = gq.export_pack([gq.Request(w, 8, 1.0)])
+    y = torch.randn(6, 40, device="cuda")
+    a = torch.randn(6, 40, device="cuda", requires_grad=True)
+    loss = (a * y).sum()
+    gq.gemm_epilogue(torch.ones(6, 64, dtype=torch.bfloat16, device="cuda"), gq.tile_weight(o.packed, 64, 8), o.scale_f16, 8,
+                     residual=y, y=y)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
