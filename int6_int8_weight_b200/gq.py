@@ -600,6 +600,21 @@ def tile_weight(packed: torch.Tensor, K: int, qbits: int, stream=None) -> torch.
     return tiles
 
 
+class _NoBackward(torch.autograd.Function):
+    """Marks ``y`` as made from ``inputs`` by a call without a backward pass: a gradient asked of it is an error, not
+    left out."""
+
+    @staticmethod
+    def forward(ctx, where, y, *inputs):
+        ctx.where = where
+        ctx.mark_dirty(y)
+        return y
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.where} has no backward pass (it runs exported weights)")
+
+
 def _rows(t, M, N):
     """The row pitch of a [M, N] tensor with contiguous rows, or None."""
     if t.shape != (M, N):
@@ -669,6 +684,10 @@ def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, o
         epi = _EPILOGUE.pack(b, r, ldr, b_code, r_code, code, y_code)
     if dev < 0 or not same or (offsets is not None and offsets.get_device() != dev):
         raise ValueError("every tensor of a call lies on one CUDA device")
+    graph = torch.is_grad_enabled() and any([t.requires_grad for t in (x, scale, bias, residual, given)
+                                             if t is not None])
+    if graph and given is not None and given.is_leaf and given.requires_grad:
+        raise ValueError("y is a leaf that requires a gradient")
     st = torch.empty(1, dtype=torch.int32, device=x.device) if check_status else None
     args = (x.data_ptr(), M, K, ldx, tiles.data_ptr(), scale.data_ptr(), qbits, N, epi, y.data_ptr(), ldy,
             None if st is None else st.data_ptr())
@@ -680,7 +699,9 @@ def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, o
         status = _on(dev, None, fn, *args)
     if status:
         _check(status, where)
-    if given is not None:
+    if graph:
+        y = _NoBackward.apply(where, y, *[t for t in (x, scale, bias, residual) if t is not None and t is not y])
+    elif given is not None:
         _written(y)
     if check_status and (v := int(st.item())):
         raise GQError(0, where, f"device status {v:#x}")
@@ -697,7 +718,8 @@ def gemm_epilogue(x: torch.Tensor, tiles: torch.Tensor, scale_f16: torch.Tensor,
     bytes, with a pitch that is a multiple of 8; ``bias`` fp32 / bf16 [N];
     ``residual`` fp32 / bf16 [M, N], may be ``y``; Y is [M, N], bf16 unless
     ``y`` or ``out_dtype`` says fp32.  ``check_status`` waits for the call and
-    raises if it gave up."""
+    raises if it gave up.  There is no backward pass: a result made from tensors
+    that require a gradient raises when one is asked of it."""
     return _layer("gq_gemm_epilogue", LIB.gq_gemm_epilogue, x, None, tiles, scale_f16, qbits, bias, act, residual, y,
                   out_dtype, stream, check_status)
 

@@ -41,6 +41,38 @@ def test_a_graph_kept_over_a_step_is_refused(gq, bits):
     assert torch.equal(x.grad, w.detach())
 
 
+@pytest.mark.parametrize("grouped", [False, True])
+def test_a_gradient_through_an_exported_layer_is_refused(gq, grouped):
+    """The layer products have no backward pass: asking for one raises instead of leaving the path out."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w = torch.randn(40, 64, device="cuda", generator=g)
+    (o,) = gq.export_pack([gq.Request(w, 6, 1.0)])
+    tiles = gq.tile_weight(o.packed, 64, 6)
+    off = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+
+    def call(x, **kw):
+        if grouped:
+            if kw.get("bias") is not None:
+                kw["bias"] = kw["bias"][None]
+            return gq.gemm_grouped(x, off, tiles[None], o.scale_f16[None], 6, **kw)
+        return gq.gemm_epilogue(x, tiles, o.scale_f16, 6, **kw)
+
+    x = torch.randn(6, 64, device="cuda", generator=g).to(torch.bfloat16)
+    want = call(x)
+    assert not want.requires_grad
+    for kw in (dict(x=x.clone().requires_grad_()), dict(x=x, bias=torch.zeros(40, device="cuda", requires_grad=True)),
+               dict(x=x, residual=torch.zeros(6, 40, device="cuda", requires_grad=True)),
+               dict(x=x.clone().requires_grad_(), y=torch.empty(6, 40, dtype=torch.bfloat16, device="cuda"))):
+        y = call(**kw)
+        assert torch.equal(y.detach(), want) and (kw.get("y") is None or y is kw["y"])
+        with pytest.raises(RuntimeError, match="no backward pass"):
+            (y.float().sum() + sum(t.float().sum() for t in kw.values() if t.is_leaf and t.requires_grad)).backward()
+        with torch.no_grad():                                  # serving: no graph
+            assert not call(**{**kw, "y": None}).requires_grad
+    with pytest.raises(ValueError):
+        call(x, y=torch.empty(6, 40, device="cuda", requires_grad=True))
+
+
 def test_a_result_in_place_of_a_saved_tensor_is_refused(gq):
     """y that a graph has saved, written over."""
     w = torch.randn(40, 64, device="cuda")
