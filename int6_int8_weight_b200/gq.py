@@ -656,7 +656,8 @@ def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, o
     if y is None:
         y_code = 1 if out_dtype is None else _DTYPE_CODES.get(out_dtype)
         if y_code is not None and same and dev >= 0:
-            y = x.new_empty((M, N), dtype=out_dtype or torch.bfloat16)
+            # (rows that belong to no expert are not written)
+            y = (x.new_empty if offsets is None else x.new_zeros)((M, N), dtype=out_dtype or torch.bfloat16)
         ldy = N
     else:
         ldy = _rows(y, M, N)
@@ -732,7 +733,8 @@ def gemm_grouped(x: torch.Tensor, offsets: torch.Tensor, tiles: torch.Tensor, sc
     rows offsets[e] .. offsets[e + 1] - 1 of ``x``, sorted by expert, use
     tiles[e], scale_f16[e] and bias[e].  ``offsets`` is int32 [E + 1] on the
     device; experts may be empty, and rows outside [offsets[0], offsets[E]) of
-    ``y`` stay as they were."""
+    ``y`` stay as they were (without ``y`` they are 0, at the cost of clearing
+    the new tensor)."""
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() \
             or offsets.shape[0] != scale_f16.shape[0] + 1:
         raise ValueError("offsets must be a contiguous int32 [E + 1] tensor")

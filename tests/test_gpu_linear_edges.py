@@ -98,3 +98,26 @@ def test_stream_refusals(gq):
         gq.gemm_epilogue(x.cpu(), W.packed[0], W.scale[0], 6, stream=torch.cuda.Stream())
     with pytest.raises(ValueError):
         gq.tile_weight(W.packed[0].cpu(), 64, 6, stream=torch.cuda.Stream())
+
+
+@pytest.mark.parametrize("first,counts,behind,K", [(3, [4, 0, 9], 20, 192), (0, [0, 0, 0], 7, 64), (1, [5, 1, 1], 2, 0),
+                                                   (2, [300, 260, 0], 60, 1600)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_rows_of_no_expert_are_zero_in_a_new_result(gq, first, counts, behind, K, out):
+    """A padded batch without a given y: memory that other tensors have left behind does not show."""
+    rng = np.random.default_rng(24)
+    M, N = first + sum(counts) + behind, 2500
+    W = Weight(gq, rng, 3, N, max(K, 1), 6)
+    tiles = gq.tile_weight(W.packed, K, 6) if K else torch.empty((3, 0), dtype=torch.uint8, device="cuda")
+    off = torch.tensor(np.concatenate([[first], first + np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    x, bias = _x(rng, M, max(K, 1))[:, :K], torch.ones((3, N), device="cuda")
+    junk = torch.full((M, N), float("nan"), dtype=out, device="cuda")
+    del junk
+    y = gq.gemm_grouped(x, off, tiles, W.scale, 6, bias=bias, out_dtype=out)
+    assert not y[:first].any() and not y[M - behind:].any()
+    for e in range(3):
+        s = slice(int(off[e]), int(off[e + 1]))
+        if s.start < s.stop and K:
+            _check(y[s], x[s], W.w[e], bias[e], None, "none", e)
+        elif s.start < s.stop:
+            assert (y[s] == 1).all()
