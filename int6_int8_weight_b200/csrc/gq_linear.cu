@@ -151,13 +151,23 @@ gq_status linear(const void* d_x, int64_t M, int64_t K, int64_t ldx, const int32
         auto size = [](int32_t d) { return d == GQ_F32 ? 4 : 2; };
         if ((K > 0 && (!aligned(d_x, 16) || (ldx % 8) != 0 || !aligned(d_tiles, 16))) || !aligned(d_scale_f16, 2) ||
             !aligned(d_y, size(e.y_dtype)) || (e.bias && !aligned(e.bias, size(e.bias_dtype))) ||
-            (e.residual && !aligned(e.residual, size(e.residual_dtype))) || !aligned(d_offsets, 4))
+            (e.residual && !aligned(e.residual, size(e.residual_dtype))))
             return GQ_ERR_MISALIGNED;
     }
+    if (!aligned(d_offsets, 4)) return GQ_ERR_MISALIGNED;
     if (d_status && cuda_status(cudaMemsetAsync(d_status, 0, sizeof(int32_t), stream)) != GQ_OK) return GQ_ERR_CUDA;
-    if (empty) return GQ_OK;
     LinParams P;
     std::memset(&P, 0, sizeof(P));
+    if (empty) {
+        // nothing to compute, but offsets that leave the batch are reported here too
+        if (!d_offsets || !d_status || E == 0) return GQ_OK;
+        P.offsets = d_offsets;
+        P.status = d_status;
+        P.M = M;
+        P.E = E;
+        linear_empty_kernel<<<1, 256, 0, stream>>>(P);     // (P.N is 0: no row is looked at)
+        return launch_status();
+    }
     P.tiles = d_tiles;
     P.scale = d_scale_f16;
     P.offsets = d_offsets;

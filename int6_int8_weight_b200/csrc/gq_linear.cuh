@@ -1103,13 +1103,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
 }
 
-// K = 0: the sums are 0, the epilogue is all there is.  One block per row of Y.
+// K = 0: the sums are 0, the epilogue is all there is.  One block per row of Y.  With N = 0: a look at the offsets alone.
 __global__ void __launch_bounds__(256) linear_empty_kernel(const __grid_constant__ LinParams P) {
     if (P.offsets && P.status && blockIdx.x == 0)
         for (int e = threadIdx.x; e < (int)P.E; e += blockDim.x) {
             const int p = P.offsets[e], q = P.offsets[e + 1];
             if (p < 0 || q < p || q > (int)P.M) atomicOr(reinterpret_cast<unsigned int*>(P.status), 0x8u);
         }
+    if (P.N == 0) return;
     for (int64_t m = blockIdx.x; m < P.M; m += gridDim.x) {
         int64_t e = 0;
         if (P.offsets) {                                   // the expert of the row: the last that begins at or before it

@@ -121,3 +121,18 @@ def test_rows_of_no_expert_are_zero_in_a_new_result(gq, first, counts, behind, K
             _check(y[s], x[s], W.w[e], bias[e], None, "none", e)
         elif s.start < s.stop:
             assert (y[s] == 1).all()
+
+
+@pytest.mark.parametrize("M,N", [(0, 130), (9, 0), (0, 0)])
+@pytest.mark.parametrize("K", [64, 0])
+def test_offsets_of_an_empty_product_are_looked_at(gq, M, N, K):
+    """No rows or no columns: offsets that leave the batch or descend are reported as anywhere else."""
+    W = Weight(gq, np.random.default_rng(25), 3, max(N, 1), 64, 6)
+    tiles = gq.tile_weight(W.packed[:, :N].contiguous(), K, 6) if K else torch.empty((3, 0), dtype=torch.uint8, device="cuda")
+    scale, x = W.scale[:, :N].contiguous(), torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    call = lambda *off: gq.gemm_grouped(x, torch.tensor(off, dtype=torch.int32, device="cuda"), tiles, scale, 6,  # noqa: E731
+                                        check_status=True)
+    assert call(0, M // 2, M // 2, M).shape == (M, N)
+    for off in ((0, 0, 0, M + 1), (-1, 0, 0, M), (0, M + 1, 0, M), (0, M, M - 1, M), (M + 1, M + 1, M + 1, M + 1)):
+        with pytest.raises(gq.GQError, match="0x8"):
+            call(*off)
