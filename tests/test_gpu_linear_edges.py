@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_linear import Weight, _check, _grouped, _run, _x
+from tests.test_gpu_linear import Weight, _check, _extra, _grouped, _run, _x
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +136,68 @@ def test_offsets_of_an_empty_product_are_looked_at(gq, M, N, K):
     for off in ((0, 0, 0, M + 1), (-1, 0, 0, M), (0, M + 1, 0, M), (0, M, M - 1, M), (M + 1, M + 1, M + 1, M + 1)):
         with pytest.raises(gq.GQError, match="0x8"):
             call(*off)
+
+
+# ------------------------------------------------------ over pairs of SMs --
+
+def _over_pairs(fn):
+    """fn() with the kernel of 256 x 256 tiles over pairs of SMs: the sizes are there to reach it, so that a change of the
+    rule that picks it does not leave it untested.  (Where the profiler sees no kernel at all this is not looked at.)"""
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as p:
+        fn()
+        torch.cuda.synchronize()
+    names = [e.name for e in p.events() if "linear" in e.name and "kernel" in e.name]
+    assert not names or any("linear_pair_kernel" in n for n in names), names
+
+
+@pytest.mark.parametrize("qbits", [6, 8])
+@pytest.mark.parametrize("M,N,K", [
+    (24001, 4865, 40), (16401, 4097, 72),                      # one stage a unit, of one and of two column blocks
+    (8193, 4225, 136), (6401, 4097, 200),                      # two
+    (6201, 4101, 320), (4101, 4097, 328),                      # three
+    (4101, 4100, 393), (3300, 4300, 505),                      # four
+    (3301, 4301, 520),                                         # five: more than there are slots
+])
+def test_pairs_with_few_stages_a_unit(gq, M, N, K, qbits):
+    """Several units a pair, with as many or fewer stages to a unit than there are slots for them: a unit's sums are
+    drained while the next units' stages are under way."""
+    _over_pairs(lambda: _run(gq, M, N, K, qbits, "silu", "f32", "bf16"))
+
+
+@pytest.mark.parametrize("N,K", [(28001, 40), (14201, 104), (8201, 136), (8201, 264), (5001, 440)])
+def test_pairs_of_experts_with_few_stages_a_unit(gq, N, K):
+    counts = [70, 0, 300, 5, 64, 200, 31, 90, 128, 1, 255, 40, 77, 33, 96, 120]
+    _over_pairs(lambda: _grouped(gq, counts, N, K, 6, "gelu_tanh", "f32", "f32", torch.bfloat16, first=1, behind=25))
+
+
+@pytest.mark.parametrize("qbits", [6, 8])
+def test_pairs_of_one_expert_among_empty_ones(gq, qbits):
+    _over_pairs(lambda: _grouped(gq, [0, 0, 900, 0], 4601, 1600, qbits, "gelu", "f32", "bf16", torch.bfloat16, first=2,
+                                 behind=40))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_pairs_with_the_residual_in_place(gq, kind):
+    rng = np.random.default_rng(26)
+    for M, N, K in ((515, 5001, 1600), (3301, 4301, 520)):
+        W = Weight(gq, rng, 1, N, K, 8)
+        x, t = _x(rng, M, K), gq.tile_weight(W.packed[0], K, 8)
+        y = _extra(rng, kind, M, N)
+        r = y.clone()
+        _over_pairs(lambda: gq.gemm_epilogue(x, t, W.scale[0], 8, act="relu2", residual=y, y=y))
+        _check(y, x, W.w[0], None, r, "relu2", (M, N, K))
+
+
+def test_an_expert_has_the_bits_of_its_own_product(gq):
+    """Same tile width and an unsplit K range in the grouped call and in each expert's own: the same bits."""
+    rng = np.random.default_rng(27)
+    for counts, N, K in (([10, 14], 19300, 200), ([16, 1, 9, 3], 19300, 136), ([100, 80], 19300, 200)):
+        W = Weight(gq, rng, len(counts), N, K, 8)
+        tiles, x = gq.tile_weight(W.packed, K, 8), _x(rng, sum(counts), K)
+        off = np.concatenate([[0], np.cumsum(counts)]).tolist()
+        y = gq.gemm_grouped(x, torch.tensor(off, dtype=torch.int32, device="cuda"), tiles, W.scale, 8, act="silu",
+                            out_dtype=torch.float32)
+        for e, (a, b) in enumerate(zip(off, off[1:])):
+            own = _x(rng, b - a, K).copy_(x[a:b])              # (a slice of x need not start on 16 bytes)
+            assert torch.equal(y[a:b], gq.gemm_epilogue(own, tiles[e], W.scale[e], 8, act="silu",
+                                                        out_dtype=torch.float32)), (counts, e)
