@@ -201,3 +201,55 @@ def test_an_expert_has_the_bits_of_its_own_product(gq):
             own = _x(rng, b - a, K).copy_(x[a:b])              # (a slice of x need not start on 16 bytes)
             assert torch.equal(y[a:b], gq.gemm_epilogue(own, tiles[e], W.scale[e], 8, act="silu",
                                                         out_dtype=torch.float32)), (counts, e)
+
+
+# ------------------------------------------------------ captured neighbours --
+
+def test_captured_between_memsets_and_joined_streams(gq):
+    """In one graph: a buffer cleared by a memset and written just before, products on two streams that join, the status
+    word of a C call, a copy behind; replayed on new inputs."""
+    rng = np.random.default_rng(28)
+    W = [Weight(gq, rng, 1, 512, 512, 6) for _ in range(3)]
+    t = [gq.tile_weight(w.packed[0], 512, 6) for w in W]
+    for M in (1, 20, 200):
+        x = torch.zeros((M, 512), dtype=torch.bfloat16, device="cuda")
+        part = torch.zeros((M, 512), dtype=torch.bfloat16, device="cuda")
+        status = torch.full((1,), 15, dtype=torch.int32, device="cuda")
+        last = torch.zeros((M, 512), dtype=torch.bfloat16, device="cuda")
+
+        def step():
+            part.zero_()
+            part[: M // 2 + 1].copy_(x[: M // 2 + 1])
+            h = gq.gemm_epilogue(part, t[0], W[0].scale[0], 6, act="silu")
+            cur = torch.cuda.current_stream()
+            side.wait_stream(cur)
+            with torch.cuda.stream(side):
+                b = gq.gemm_epilogue(h, t[1], W[1].scale[0], 6, act="gelu")
+                b.zero_() if M == 20 else b.mul_(0.5)
+                b = gq.gemm_epilogue(x, t[1], W[1].scale[0], 6, residual=b, y=b)
+            a = gq.gemm_epilogue(h, t[2], W[2].scale[0], 6, act="relu")
+            cur.wait_stream(side)
+            b.record_stream(cur)
+            e = gq.GQEpilogue(residual=b.data_ptr(), ldr=512, residual_dtype=1, y_dtype=1)
+            y = torch.zeros_like(x)
+            assert gq.LIB.gq_gemm_epilogue(a.data_ptr(), M, 512, 512, t[0].data_ptr(), W[0].scale.data_ptr(), 6, 512,
+                                           gq.C.byref(e), y.data_ptr(), 512, status.data_ptr(), cur.cuda_stream) == 0
+            last.copy_(y)
+            return a, b, y
+
+        side = torch.cuda.Stream()
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for seed in range(3):
+            x.copy_(_x(np.random.default_rng(seed), M, 512))
+            step()
+            torch.cuda.synchronize()
+            want = last.clone()
+            last.zero_(), status.fill_(15)
+            for _ in range(2):
+                graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(last, want) and status.item() == 0 and last.any()
