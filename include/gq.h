@@ -534,21 +534,35 @@ GQ_API gq_status gq_gemm_grouped(const void* d_x, int64_t M, int64_t K, int64_t 
  * to nearest even bf16.  Every output is bit-exact to that definition.
  *
  * States: binary32 m and v (state_bits 32), or 8 bits each with binary32
- * scales per block of 256 consecutive elements (state_bits 8):
- *   m = RN(qm * sm), qm int8 in [-127, 127];  v = RN(RN(qv^2)^2 * sv), qv uint8
- * (a fourth power: v spans nine decades of a block, the codes densest
- * where the block's large values lie).  New codes, with a = max |m'| (max v')
- * of the block and f(q) = RN((q^2)^2):
- *   sm = RN(a * RN(1 / 127)), x = RN(m' * RN(127 / a)), qm = clamp(floor(RN(x + u1)), -127, 127)
+ * scales per block of 256 consecutive elements.  v is a fourth power, v = RN(RN(qv^2)^2 * sv),
+ * qv uint8 (it spans nine decades of a block, the codes densest where the
+ * block's large values lie); m, qm int8 in [-127, 127], is
+ *   m = RN(qm * sm)            linear codes (state_bits 8), or
+ *   m = RN(qm * |qm| * sm)     square codes (GQ_ADAMW_8_SQUARE).
+ * New codes, with a = max |m'| (max v') of the block and f(q) = RN((q^2)^2):
+ *   linear: sm = RN(a * RN(1 / 127)), x = RN(m' * RN(127 / a)), qm = clamp(floor(RN(x + u1)), -127, 127)
+ *   square: sm = RN(a * RN(1 / 127^2)), x = RN(|m'| * RN(127^2 / a)), q0 = the largest q <= 126 with q^2 <= x,
+ *           |qm| = q0 + (u1 * (2 q0 + 1) < RN(x - q0^2)), the sign that of m'
  *   sv = RN(a * RN(1 / 255^4)), x = RN(v' * RN(255^4 / a)), q0 = the largest q <= 254 with f(q) <= x,
  *   qv = q0 + (RN(u2 * RN(f(q0 + 1) - f(q0))) < RN(x - f(q0))), and 1 where that is 0 but x > 0;
  *   a < 2^-80 gives scale 0 and codes 0.
  * u1, u2 are 16 random bits each (k * 2^-16) from a hash of the element's
- * index, the tensor's place in the batch, the step and the seed: rounding is
- * unbiased, so that changes of a state smaller than a code's step are not
- * lost, and reproducible.  (An m far below its block's largest is stored as 0
- * or as a whole code step, the mean being right: such an element moves seldom
- * and then by more than the 32-bit step would move it.)
+ * index, the tensor's place in the batch, the step and the seed: reproducible, and
+ * m's mean and that of v above its first code are right to 2^-16 of a code's step, so that
+ * changes of a state smaller than that step are not lost.  (v below its
+ * first code is stored as that code, above its value, since the step divides by its root.)
+ *
+ * Which codes: an element far below its block's largest keeps v to a / 255^4 but, in linear codes, m only
+ * as 0 or a whole a / 127, and then moves by many times lr in one step; square codes step as
+ * sqrt(v) = qv^2 * sqrt(sv) does.  Largest |update| / lr (and root mean square) over 200 steps, b = (0.9, 0.95), gradients
+ * N(0, 1) times a scale of each element's own; 32-bit states: 1.0 (0.26) throughout:
+ *   scales in a block          linear         square
+ *   equal                      1.3 (0.26)     1.0 (0.26)
+ *   exp(N(0, 1))               4.5 (0.27)     1.2 (0.26)
+ *   one 1000 times the rest    32  (1.14)     2.7 (0.29)
+ *   exp(2 N(0, 1))             279 (2.0)      27  (0.34)
+ * So: square codes, except for states that exist in linear ones; and 32-bit
+ * states where gradients within 256 neighbours differ by many powers of ten.
  *
  * t[i]: p (fp32 / bf16), g (fp32 / bf16), m, v dense arrays of numel elements;
  * m_scale, v_scale [ceil(numel / 256)] for 8-bit states, else NULL; p_copy
@@ -565,6 +579,8 @@ GQ_API gq_status gq_gemm_grouped(const void* d_x, int64_t M, int64_t K, int64_t 
  * Asynchronous on `stream`, no workspace; one launch per 200 tensors of a state size.
  * Source: AdamW with decoupled weight decay (PR #69, PR #1414).
  */
+#define GQ_ADAMW_8_SQUARE 0x108   /* state_bits: 8-bit states, the first moment in square codes */
+
 typedef struct gq_adamw_tensor {
     void* p;
     const void* g;
@@ -576,7 +592,7 @@ typedef struct gq_adamw_tensor {
     int64_t numel;
     int32_t p_dtype;
     int32_t g_dtype;
-    int32_t state_bits;       /* 32 or 8 */
+    int32_t state_bits;       /* 32, 8 or GQ_ADAMW_8_SQUARE */
     int32_t reserved;         /* must be 0 */
     double weight_decay;
 } gq_adamw_tensor;

@@ -14,17 +14,24 @@ static_assert(sizeof(gq_adamw_tensor) == 88 && sizeof(gq_adamw_hyper) == 72,
               "the layouts are part of the ABI (the Python binding mirrors them)");
 static_assert(sizeof(AdamParams<kAdamDesc>) <= 32764, "kernel parameters end at 32764 bytes");
 
+// The states of a tensor, -1 where state_bits is none of them.
+int adam_state(const gq_adamw_tensor& t) {
+    return t.state_bits == 32 ? kAdam32 : t.state_bits == 8 ? kAdam8Linear
+         : t.state_bits == GQ_ADAMW_8_SQUARE ? kAdam8Square : -1;
+}
+
 gq_status check_adamw(const gq_adamw_tensor& t) {
     if (t.reserved != 0 || t.numel < 0) return GQ_ERR_INVALID_ARG;
     if ((t.p_dtype != GQ_F32 && t.p_dtype != GQ_BF16) || (t.g_dtype != GQ_F32 && t.g_dtype != GQ_BF16))
         return GQ_ERR_INVALID_ARG;
-    if (t.state_bits != 32 && t.state_bits != 8) return GQ_ERR_INVALID_ARG;
+    if (adam_state(t) < 0) return GQ_ERR_INVALID_ARG;
+    const bool s8 = t.state_bits != 32;
     if (!std::isfinite(t.weight_decay)) return GQ_ERR_INVALID_ARG;
     if (t.numel > INT64_MAX / 16) return GQ_ERR_INVALID_ARG;
     if (t.numel == 0) return GQ_OK;
     if (!t.p || !t.g || !t.m || !t.v) return GQ_ERR_INVALID_ARG;
-    if (t.state_bits == 8 ? (!t.m_scale || !t.v_scale) : (t.m_scale || t.v_scale)) return GQ_ERR_INVALID_ARG;
-    const size_t ps = t.p_dtype == GQ_F32 ? 4 : 2, gs = t.g_dtype == GQ_F32 ? 4 : 2, ss = t.state_bits / 8;
+    if (s8 ? (!t.m_scale || !t.v_scale) : (t.m_scale || t.v_scale)) return GQ_ERR_INVALID_ARG;
+    const size_t ps = t.p_dtype == GQ_F32 ? 4 : 2, gs = t.g_dtype == GQ_F32 ? 4 : 2, ss = s8 ? 1 : 4;
     if (!aligned(t.p, ps) || !aligned(t.g, gs) || !aligned(t.m, ss) || !aligned(t.v, ss) ||
         (t.p_copy && !aligned(t.p_copy, 2)) || (t.m_scale && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
         return GQ_ERR_MISALIGNED;
@@ -36,15 +43,16 @@ template <int CAP>
 gq_status launch_adamw(const gq_adamw_tensor* t, int n, const gq_adamw_hyper* h, const AdamStep& S, cudaStream_t stream) {
     AdamParams<CAP> P;
     static_cast<AdamStep&>(P) = S;
-    // the tensors with 8-bit states and those with 32-bit ones, up to CAP a launch
-    for (const bool s8 : {false, true}) {
+    // the tensors of each kind of states, up to CAP a launch
+    for (const int state : {kAdam32, kAdam8Linear, kAdam8Square}) {
+        const bool s8 = state != kAdam32;
         int i = 0;
         while (i < n) {
             int64_t items = 0;
             P.ndesc = 0;
             for (; i < n && P.ndesc < CAP; ++i) {
                 const gq_adamw_tensor& T = t[i];
-                if (T.numel == 0 || (T.state_bits == 8) != s8) continue;
+                if (T.numel == 0 || adam_state(T) != state) continue;
                 AdamDesc& D = P.d[P.ndesc];
                 D.p = T.p;
                 D.g = T.g;
@@ -69,8 +77,9 @@ gq_status launch_adamw(const gq_adamw_tensor* t, int n, const gq_adamw_hyper* h,
             P.start[P.ndesc] = items;
             if (items == 0) continue;
             const unsigned blocks = (unsigned)std::min<int64_t>(items, (int64_t)sm_count() * 32);
-            if (s8) adamw_kernel<true, CAP><<<blocks, kAdamThreads, 0, stream>>>(P);
-            else adamw_kernel<false, CAP><<<blocks, kAdamThreads, 0, stream>>>(P);
+            if (state == kAdam32) adamw_kernel<kAdam32, CAP><<<blocks, kAdamThreads, 0, stream>>>(P);
+            else if (state == kAdam8Linear) adamw_kernel<kAdam8Linear, CAP><<<blocks, kAdamThreads, 0, stream>>>(P);
+            else adamw_kernel<kAdam8Square, CAP><<<blocks, kAdamThreads, 0, stream>>>(P);
             if (launch_status() != GQ_OK) return GQ_ERR_CUDA;
         }
     }

@@ -239,9 +239,13 @@ __device__ __forceinline__ void adam_store8(const uint32_t (&c)[2], void* base, 
     }
 }
 
-// S8: the launch's tensors have 8-bit states.
-template <bool S8, int CAP>
-__global__ void __launch_bounds__(kAdamThreads, S8 ? 5 : 4) adamw_kernel(const __grid_constant__ AdamParams<CAP> P) {
+// What the launch's tensors hold as states: 32 bits, or 8 with the first moment in linear or in square codes.
+enum AdamState { kAdam32, kAdam8Linear, kAdam8Square };
+
+template <int ST, int CAP>
+__global__ void __launch_bounds__(kAdamThreads, ST == kAdam32 ? 4 : 5)
+    adamw_kernel(const __grid_constant__ AdamParams<CAP> P) {
+    constexpr bool S8 = ST != kAdam32;
     __shared__ float s_step[3];
     float inv_bc2 = P.inv_bc2, step_size = P.step_size;
     double lr = P.lr;
@@ -304,7 +308,13 @@ __global__ void __launch_bounds__(kAdamThreads, S8 ? 5 : 4) adamw_kernel(const _
             for (int i = 0; i < 8; i += 2) {
                 const AdamF2 qm = U.add(bytes(cm[i >> 2] ^ 0x80808080u, i & 3), adam2(-8388736.0f));
                 const AdamF2 qv = U.add(bytes(cv[i >> 2], i & 3), adam2(-8388608.0f));
-                adam2_out(adam2_mul(qm, adam2(ms)), m[i], m[i + 1]);
+                if constexpr (ST == kAdam8Square) {
+                    float q0, q1;
+                    adam2_out(qm, q0, q1);
+                    adam2_out(adam2_mul(adam2_mul(qm, adam2(fabsf(q0), fabsf(q1))), adam2(ms)), m[i], m[i + 1]);
+                } else {
+                    adam2_out(adam2_mul(qm, adam2(ms)), m[i], m[i + 1]);
+                }
                 adam2_out(adam2_mul(adam2_fourth(qv), adam2(vs)), v[i], v[i + 1]);
             }
         } else {
@@ -363,7 +373,7 @@ __global__ void __launch_bounds__(kAdamThreads, S8 ? 5 : 4) adamw_kernel(const _
         am = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(am)));   // non-negative: ordered like their bits
         av = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(av)));
         const bool km = am >= kAdamTiny, kv = av >= kAdamTiny;
-        const float im = km ? __fdiv_rn(127.0f, am) : 0.0f;
+        const float im = km ? __fdiv_rn(ST == kAdam8Square ? 16129.0f : 127.0f, am) : 0.0f;   // 127^2
         const float iv = kv ? __fdiv_rn(4228250625.0f, av) : 0.0f;   // 255^4
         uint32_t cm[2] = {0u, 0u}, cv[2] = {0u, 0u};
         const uint32_t z0 = adam_seed(e, D.key + key_step);
@@ -378,11 +388,34 @@ __global__ void __launch_bounds__(kAdamThreads, S8 ? 5 : 4) adamw_kernel(const _
                                  adam2(1.52587890625e-5f), adam2(-128.0f));
             };
             const AdamF2 um = unit(za, zb, 0x7432), uv = unit(za, zb, 0x7410);
-            // floor by an addition rounded down: the code is in the low byte of the sum's bits (it is at most 127:
-            // m' * RN(127 / a) is below 127 + 2^-15, and u at most 1 - 2^-16)
             float t0, t1;
-            adam2_out(U.add(adam2_mul(adam2(m[i], m[i + 1]), adam2(im)), um), t0, t1);
-            adam2_out(U.add_down(adam2(fmaxf(t0, -127.0f), fmaxf(t1, -127.0f)), adam2(kMagic)), t0, t1);
+            if constexpr (ST == kAdam8Square) {
+                // |q| = q0 + (u (2 q0 + 1) < x - q0^2): q0 as the fourth root's below, from one root; 16 + 8 bits of
+                // u (2 q0 + 1) are exact.  The sum with kMagic holds the signed code in its low byte.
+                const AdamF2 x = adam2_mul(adam2(fabsf(m[i]), fabsf(m[i + 1])), adam2(im));
+                float x0, x1, q0, q1, f0, f1;
+                adam2_out(x, x0, x1);
+                adam2_out(adam2_mul(adam2(adam_root(x0), adam_root(x1)), adam2(1.000003814697265625f)), q0, q1);
+                AdamF2 q = U.add(U.add_down(adam2(fminf(q0, 126.0f), fminf(q1, 126.0f)), adam2(8388608.0f)),
+                                 adam2(-8388608.0f));
+                AdamF2 f = adam2_mul(q, q);
+                adam2_out(f, f0, f1);
+                if (f0 > x0 || f1 > x1) {
+                    adam2_out(q, q0, q1);
+                    q = adam2(f0 > x0 ? q0 - 1.0f : q0, f1 > x1 ? q1 - 1.0f : q1);
+                    f = adam2_mul(q, q);
+                }
+                float s0, s1, r0, r1;
+                adam2_out(adam2_mul(um, adam2_fma(q, adam2(2.0f), U.one)), s0, s1);
+                adam2_out(U.sub(x, f), r0, r1);
+                adam2_out(U.add(q, adam2(s0 < r0 ? 1.0f : 0.0f, s1 < r1 ? 1.0f : 0.0f)), q0, q1);
+                adam2_out(U.add(adam2(copysignf(q0, m[i]), copysignf(q1, m[i + 1])), adam2(kMagic)), t0, t1);
+            } else {
+                // floor by an addition rounded down: the code is in the low byte of the sum's bits (it is at most 127:
+                // m' * RN(127 / a) is below 127 + 2^-15, and u at most 1 - 2^-16)
+                adam2_out(U.add(adam2_mul(adam2(m[i], m[i + 1]), adam2(im)), um), t0, t1);
+                adam2_out(U.add_down(adam2(fmaxf(t0, -127.0f), fmaxf(t1, -127.0f)), adam2(kMagic)), t0, t1);
+            }
             const AdamF2 x = adam2_mul(adam2(v[i], v[i + 1]), adam2(iv));
             float x0, x1, q0, q1, f0, f1;
             adam2_out(x, x0, x1);
@@ -415,7 +448,8 @@ __global__ void __launch_bounds__(kAdamThreads, S8 ? 5 : 4) adamw_kernel(const _
         adam_store8(cm, D.m, e, n, vec);
         adam_store8(cv, D.v, e, n, vec);
         if (lane == 0) {
-            D.ms[blk] = km ? __fmul_rn(am, 0.007874015748031496f) : 0.0f;       // RN(1 / 127)
+            // RN(1 / 127), RN(1 / 127^2)
+            D.ms[blk] = km ? __fmul_rn(am, ST == kAdam8Square ? 6.200012400024800e-05f : 0.007874015748031496f) : 0.0f;
             D.vs[blk] = kv ? __fmul_rn(av, 2.3650442906278766e-10f) : 0.0f;     // RN(1 / 255^4)
         }
     }

@@ -37,6 +37,7 @@ GQ_SCALE_F32, GQ_SCALE_F16 = 0, 1
 GQ_STATUS_NONFINITE, GQ_STATUS_RANGE, GQ_STATUS_TIMEOUT, GQ_STATUS_OFFSETS = 1, 2, 4, 8
 ACTS = {"none": 0, "relu": 1, "relu2": 2, "leaky_relu2": 3, "silu": 4, "gelu": 5, "gelu_tanh": 6}
 ADAMW_BLOCK = 256                # elements that share an 8-bit state's scale
+ADAMW_CODES = {"linear": 8, "square": 0x108}   # state_bits of 8-bit states by the first moment's codes
 GQ_AVG_MEAN, GQ_AVG_EMA = 0, 1
 GQ_KIND_RAW, GQ_KIND_FP16, GQ_KIND_INT8, GQ_KIND_INT6 = 0, 1, 2, 3
 KIND_NAMES = {GQ_KIND_RAW: "raw", GQ_KIND_FP16: "fp16", GQ_KIND_INT8: "int8", GQ_KIND_INT6: "int6"}
@@ -755,12 +756,15 @@ def _scalar(name, value, dtype, dev) -> int:
 
 def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
                weight_decay=0.01, scales=None, copies=None, grad_scale: torch.Tensor | None = None, seed: int = 0,
-               stream=None) -> None:
+               stream=None, codes: str = "linear") -> None:
     """One AdamW step over lists of tensors, in place (gq_adamw_step).
 
     ``params`` / ``grads`` fp32 or bf16; ``exp_avgs`` / ``exp_avg_sqs`` fp32, or
     int8 / uint8 codes with ``scales`` = (lists of) their fp32 block scales
-    [ceil(numel / 256)] (all zeros at the start); ``copies`` bf16 copies of the
+    [ceil(numel / 256)] (all zeros at the start), the first moment's ``codes``
+    "linear" or "square" (the same throughout a run; square ones keep an element
+    whose gradients are far below its neighbours' from steps of many times
+    ``lr``, see gq_adamw_step); ``copies`` bf16 copies of the
     new weights (a list, entries may be None).  ``step`` (from 1) and ``lr`` are
     numbers, or int64 / fp32 tensors on the device that a captured step reads
     when it is replayed.  A weight is listed once.  ``weight_decay``: one number or one per tensor.
@@ -770,9 +774,11 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     if n == 0 and not (len(grads) or len(exp_avgs) or len(exp_avg_sqs)):
         return
     # all tensors at a time: a loop over them would take longer than the step of a small model
-    bits = 32 if scales is None else 8
+    bits = 32 if scales is None else ADAMW_CODES.get(codes)
+    if bits is None or (scales is None and codes != "linear"):
+        raise ValueError("codes of 8-bit states are linear or square")
     lists = [params, grads, exp_avgs, exp_avg_sqs]
-    if bits == 8:
+    if bits != 32:
         lists += scales
     if len(lists) not in (4, 6) or any(len(ts) != n for ts in lists) or (copies is not None and len(copies) != n):
         raise ValueError("params, grads, states, scales and copies are lists of one length")
@@ -787,14 +793,14 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     if sizes[n:4 * n] != numel * 3:
         raise ValueError("weights, gradients and states are of one size")
     try:
-        codes = [_DTYPE_CODES[k] for k in dtypes[:2 * n]]
+        kinds = [_DTYPE_CODES[k] for k in dtypes[:2 * n]]
     except KeyError as e:
         raise TypeError(f"weights and gradients are float32 or bfloat16, got {e.args[0]}") from None
     if set(dtypes[2 * n:3 * n]) != {torch.float32 if bits == 32 else torch.int8} \
             or set(dtypes[3 * n:4 * n]) != {torch.float32 if bits == 32 else torch.uint8}:
         raise TypeError("states are fp32, or int8 / uint8 codes with scales")
-    if bits == 8 and (sizes[4 * n:] != [-(-k // ADAMW_BLOCK) for k in numel] * 2
-                      or set(dtypes[4 * n:]) != {torch.float32}):
+    if bits != 32 and (sizes[4 * n:] != [-(-k // ADAMW_BLOCK) for k in numel] * 2
+                       or set(dtypes[4 * n:]) != {torch.float32}):
         raise ValueError("scales are contiguous fp32 tensors of ceil(numel / 256) elements")
     copy = repeat(0)
     if copies is not None:
@@ -808,7 +814,7 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
         raise ValueError("weight_decay is a number or one per tensor")
     ptr = list(map(_data_ptr, flat))
     pointers = [ptr[i:i + n] for i in range(0, len(ptr), n)] + [repeat(0)] * (6 - len(lists))
-    desc = b"".join(map(_ADAMW_TENSOR.pack, *pointers, copy, numel, codes[:n], codes[n:], repeat(bits), repeat(0),
+    desc = b"".join(map(_ADAMW_TENSOR.pack, *pointers, copy, numel, kinds[:n], kinds[n:], repeat(bits), repeat(0),
                         repeat(weight_decay) if one else weight_decay))
     d_step, d_lr = _scalar("step", step, torch.int64, dev), _scalar("lr", lr, torch.float32, dev)
     d_scale = 0 if grad_scale is None else _scalar("grad_scale", grad_scale, torch.float32, dev)

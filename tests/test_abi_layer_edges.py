@@ -24,3 +24,20 @@ def test_offsets_of_an_empty_product_are_aligned(gq, M, N, E, code):
     assert gq.LIB.gq_gemm_grouped(*args, O + 64, None) == code
     assert gq.LIB.gq_gemm_grouped(*args, None, None) == code
     assert gq.LIB.gq_gemm_grouped(*args[:4], O, *args[5:], None, None) == 0
+
+
+def test_kinds_of_adamw_states(gq):
+    """8-bit states with square codes want their scales like those with linear ones; other values of state_bits are none."""
+    def call(**kw):
+        t = gq.GQAdamWTensor(**{**dict(p=X, g=T, m=S + 1, v=Y + 3, numel=8), **kw})
+        h = gq.GQAdamWHyper(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1)
+        return gq.LIB.gq_adamw_step(C.byref(t), 1, C.byref(h), None)
+
+    square = gq.ADAMW_CODES["square"]
+    assert square == 0x108 and gq.ADAMW_CODES["linear"] == 8
+    assert call(state_bits=square) == 1 and call(state_bits=square, m_scale=O) == 1
+    assert call(state_bits=square, m_scale=O, v_scale=O + 2) == 3
+    assert call(state_bits=square, m_scale=O, v_scale=O, reserved=1) == 1
+    assert call(state_bits=square, m_scale=O, v_scale=O, numel=0) == 0
+    for bits in (0, 7, 264 + 8, 0x208, 0x120, -8):
+        assert call(state_bits=bits, m_scale=O, v_scale=O) == 1
