@@ -576,7 +576,7 @@ _ADAMW_TENSOR = struct.Struct("@PPPPPPPqiiiid")              # gq_adamw_tensor
 _ADAMW_HYPER = struct.Struct("@ddddqQPPP")                   # gq_adamw_hyper
 _numel, _is_contiguous, _get_device = torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.get_device
 _data_ptr, _get_dtype = torch.Tensor.data_ptr, attrgetter("dtype")
-_written = torch.autograd.graph.increment_version          # of tensors that a kernel wrote in place
+_written = torch.autograd.graph.increment_version          # of a list of tensors that a kernel wrote in place
 _EPILOGUE = struct.Struct("@PPqiiii")                      # gq_epilogue
 _EPILOGUE_NONE = {(a, y): _EPILOGUE.pack(0, 0, 0, 0, 0, a, y) for a in ACTS.values() for y in (GQ_F32, GQ_BF16)}
 
@@ -686,8 +686,9 @@ def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, o
         epi = _EPILOGUE.pack(b, r, ldr, b_code, r_code, code, y_code)
     if dev < 0 or not same or (offsets is not None and offsets.get_device() != dev):
         raise ValueError("every tensor of a call lies on one CUDA device")
-    graph = torch.is_grad_enabled() and any([t.requires_grad for t in (x, scale, bias, residual, given)
-                                             if t is not None])
+    graph = torch.is_grad_enabled() and (
+        x.requires_grad or scale.requires_grad or (bias is not None and bias.requires_grad)
+        or (residual is not None and residual.requires_grad) or (given is not None and given.requires_grad))
     if graph and given is not None and given.is_leaf and given.requires_grad:
         raise ValueError("y is a leaf that requires a gradient")
     st = torch.empty(1, dtype=torch.int32, device=x.device) if check_status else None
@@ -704,7 +705,7 @@ def _layer(where, fn, x, offsets, tiles, scale, qbits, bias, act, residual, y, o
     if graph:
         y = _NoBackward.apply(where, y, *[t for t in (x, scale, bias, residual) if t is not None and t is not y])
     elif given is not None:
-        _written(y)
+        _written((y,))
     if check_status and (v := int(st.item())):
         raise GQError(0, where, f"device status {v:#x}")
     return y
@@ -792,15 +793,19 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
     numel = sizes[:n]
     if sizes[n:4 * n] != numel * 3:
         raise ValueError("weights, gradients and states are of one size")
-    try:
-        kinds = [_DTYPE_CODES[k] for k in dtypes[:2 * n]]
-    except KeyError as e:
-        raise TypeError(f"weights and gradients are float32 or bfloat16, got {e.args[0]}") from None
-    if set(dtypes[2 * n:3 * n]) != {torch.float32 if bits == 32 else torch.int8} \
-            or set(dtypes[3 * n:4 * n]) != {torch.float32 if bits == 32 else torch.uint8}:
+    # (counting compares by identity, which takes a fraction of hashing the types)
+    if dtypes[:2 * n].count(torch.float32) == 2 * n:
+        kinds = [GQ_F32] * (2 * n)
+    else:
+        try:
+            kinds = [_DTYPE_CODES[k] for k in dtypes[:2 * n]]
+        except KeyError as e:
+            raise TypeError(f"weights and gradients are float32 or bfloat16, got {e.args[0]}") from None
+    if dtypes[2 * n:3 * n].count(torch.float32 if bits == 32 else torch.int8) != n \
+            or dtypes[3 * n:4 * n].count(torch.float32 if bits == 32 else torch.uint8) != n:
         raise TypeError("states are fp32, or int8 / uint8 codes with scales")
     if bits != 32 and (sizes[4 * n:] != [-(-k // ADAMW_BLOCK) for k in numel] * 2
-                       or set(dtypes[4 * n:]) != {torch.float32}):
+                       or dtypes[4 * n:].count(torch.float32) != 2 * n):
         raise ValueError("scales are contiguous fp32 tensors of ceil(numel / 256) elements")
     copy = repeat(0)
     if copies is not None:
@@ -822,8 +827,7 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, step, lr, betas=(0.9, 0.999
                           d_scale)
     _check(_on(dev, stream, LIB.gq_adamw_step, desc, n, GQAdamWHyper.from_buffer_copy(h)), "gq_adamw_step")
     # written behind autograd's back: a graph that saved one of them is not to be run backwards any more
-    _written(flat[:n])
-    _written(flat[2 * n:])
+    _written(flat[:n] + flat[2 * n:])
     if copies is not None:
         _written([c for c in copies if c is not None])
 
