@@ -367,6 +367,23 @@ class _Scratch:
 _SCRATCH = _Scratch()
 
 
+def _stream_of(stream, index: int) -> torch.cuda.Stream:
+    """``stream`` (a torch stream, a handle or an object that has one) as a torch stream of device ``index``."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=index)
+    if stream.device_index != index:
+        raise ValueError("the stream is one of the tensors' device")
+    return stream
+
+
+def _status_values(st: torch.Tensor, n: int, stream) -> list:
+    """The first ``n`` status words, read on the stream that the call runs on."""
+    if stream is None:
+        return st[:n].cpu().tolist()
+    with torch.cuda.stream(_stream_of(stream, st.get_device())):
+        return st[:n].cpu().tolist()
+
+
 def _run(fn_name, reqs, export, mode=None, stream=None, check_status=True, avgs=None):
     if not reqs:
         return []
@@ -386,8 +403,7 @@ def _run(fn_name, reqs, export, mode=None, stream=None, check_status=True, avgs=
     else:
         gq_row_clip_select(descs, **args)
     if check_status:
-        stv = st[: len(descs)].cpu().tolist()
-        for o, s in zip(outs, stv):
+        for o, s in zip(outs, _status_values(st, len(descs), stream)):
             o.status = int(s)
     return outs
 
@@ -488,7 +504,7 @@ def gptq_quantize(req: Request, H: torch.Tensor, percdamp: float = 0.01, stream=
     _check(LIB.gq_gptq_quantize(C.byref(d), H.data_ptr(), float(percdamp), ws.data_ptr(), ws.numel(),
                                 st.data_ptr(), _stream(stream)), "gq_gptq_quantize")
     if check_status:
-        o.status = int(st[0].item())
+        o.status = int(_status_values(st, 1, stream)[0])
     return o
 
 
@@ -518,8 +534,7 @@ def gptq_quantize_batch(reqs, Hs, percdamp: float = 0.01, stream=None,
     _check(LIB.gq_gptq_quantize_batch(arr, len(descs), hp, float(percdamp), ws.data_ptr(), ws.numel(),
                                       st.data_ptr(), _stream(stream)), "gq_gptq_quantize_batch")
     if check_status:
-        sv = st[:len(descs)].cpu().tolist()
-        for o, v in zip(outs, sv):
+        for o, v in zip(outs, _status_values(st, len(descs), stream)):
             o.status = int(v)
     return outs
 
@@ -560,11 +575,7 @@ def _on_given(stream, index: int, y, fn, *args) -> torch.Tensor:
     is kept for the caller's own stream too, which is to use it."""
     if index < 0:
         raise ValueError("libgq takes CUDA tensors")
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=index)
-    if stream.device_index != index:
-        raise ValueError("the stream is one of the tensors' device")
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_stream_of(stream, index)):
         out = fn(*args)
     if y is None:
         out.record_stream(torch.cuda.current_stream(index))
