@@ -473,8 +473,11 @@ GQ_API gq_status gq_gemm_fakequant(const void* d_x, int64_t M, int64_t K, int64_
  * act(bias) + residual.  No workspace; Y is the same bits on every call with
  * the same arguments (no atomics: a K range split over blocks is summed in a
  * fixed order).  |Z - exact| <= (K/8 + 32) * 2^-24 * sum_k |X * W| plus one
- * binary32 rounding for scale and bias together; silu and the gelus are good to
- * a few units in the last place of max(|z|, 1).
+ * binary32 rounding for scale and bias together, while sum_k |X * q| stays
+ * within binary32 (the scale comes after the sum, which is infinite beyond that
+ * even where Z would not be); silu and the gelus, for binary32 Y too, are good to
+ * 3 units of 2^-24 max(|z|, 1): an error that is absolute where |z| < 1 and in gelu's negative
+ * tail, where the value itself is far smaller.
  * NaN and infinities of X, bias and residual propagate as in those formulas
  * (relu(NaN) = NaN).
  *
@@ -531,7 +534,10 @@ GQ_API gq_status gq_gemm_grouped(const void* d_x, int64_t M, int64_t K, int64_t 
  *   p' = RN(RN(p * RN(1 - lr * wd)) - RN(RN(m' / d) * RN(lr / (1 - b1^t))))
  * in binary32 (the scalars in binary64, each rounded once; products such as
  * lr * wd are in binary64); a bf16 weight is widened exactly and p' rounded
- * to nearest even bf16.  Every output is bit-exact to that definition.
+ * to nearest even bf16.  Every output is bit-exact to that definition.  (b1^t and b2^t
+ * are binary64 powers of the host's library or, with d_step, of the device's; where they
+ * differ in their last bits one of the two scalars may round to the next binary32,
+ * at most about once in 10^5 steps.)
  *
  * States: binary32 m and v (state_bits 32), or 8 bits each with binary32
  * scales per block of 256 consecutive elements.  v is a fourth power, v = RN(RN(qv^2)^2 * sv),
@@ -576,7 +582,7 @@ GQ_API gq_status gq_gemm_grouped(const void* d_x, int64_t M, int64_t K, int64_t 
  * A non-finite gradient reaches p, m and v as the formulas say (32-bit); in an
  * 8-bit block whose m' or v' has a NaN or an infinity the new codes and
  * scales of that block are unspecified.
- * Asynchronous on `stream`, no workspace; one launch per 200 tensors of a state size.
+ * Asynchronous on `stream`, no workspace; one launch per 200 tensors of a kind of states.
  * Source: AdamW with decoupled weight decay (PR #69, PR #1414).
  */
 #define GQ_ADAMW_8_SQUARE 0x108   /* state_bits: 8-bit states, the first moment in square codes */

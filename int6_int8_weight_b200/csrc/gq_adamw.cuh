@@ -6,9 +6,10 @@
 // fp32 weights and states, 10 with bf16 weights and 8-bit states.  Bound with
 // 32-bit states: HBM (the weights of 9 layers of d 512, 606 MB in all, in 93 us:
 // 6.5 TB/s).  With 8-bit states the square root, the quotient,
-// the fourth root and the hash come to about 90 instructions an element, and
-// their issue is the bound: 16384 x 8192 bf16 in 449 us, 3.0 TB/s, 70 % of the
-// issue slots.
+// the fourth root and the hash come to 90 instructions an element, 104 with the
+// first moment in square codes, and their issue is the bound: 16384 x 8192, fp32
+// weights and bf16 gradients, in 451 us (4.2 TB/s), 506 with square codes, at 70 % of the
+// issue slots.  48 registers (five blocks an SM) leave 36 bytes of spills.
 //
 // Split: a work item is a run of 2048 elements of one tensor (8 blocks of 256,
 // one a warp), so that any list of tensors spreads evenly; a lane owns 8
@@ -69,8 +70,11 @@ struct AdamParams : AdamStep {
 
 constexpr uint32_t kAdamStepMul = 0x632BE5ABu, kAdamTensorMul = 0x2C1B3C6Du;
 
-// 32 random bits of an element: two multiply-xorshift rounds over a seed that
-// moves by a constant with the index.
+// 32 random bits of an element: two multiply-xorshift rounds over a seed that moves
+// with the index by 2^32 / golden ratio (Knuth's multiplicative hashing).  The
+// rounds' shifts and multipliers are a result of C. Wellons' published search for
+// 32-bit mixers of low bias ("Prospecting for Hash Functions", 2018); the other
+// constants only keep steps, tensors and high index words apart.
 __device__ __forceinline__ uint32_t adam_seed(int64_t index, uint32_t key) {
     return (uint32_t)index * 0x9E3779B9u + (uint32_t)((uint64_t)index >> 32) * 0x7FEB3529u + key;
 }

@@ -28,8 +28,10 @@ constexpr int kLinK = 64;
 __host__ __device__ constexpr int lin_block_bytes(int qbits) { return kLinRows * (qbits == 6 ? 48 : 64); }
 
 // One thread per row of a block: 64 codes of the packed row in, 48 / 64 bytes of
-// the tile out.  Bound: HBM, once per weight; the packed rows may start at any
-// byte, so they are read byte by byte (through L1).
+// the tile out.  The packed rows may start at any byte, so they are read byte by
+// byte, and the lanes of a warp read a row pitch apart: bound by those loads
+// (16384 x 16384: 1420 us int6, 966 int8; its bytes once in and out would be 61
+// and 82).  It runs once per weight, when that is exported or loaded.
 __global__ void __launch_bounds__(kLinRows) tile_weight_kernel(const uint8_t* __restrict__ packed, int64_t N, int64_t K,
                                                                int64_t prb, int qbits, int64_t kbs, uint8_t* tiles) {
     const int64_t block = blockIdx.x;                      // (expert, row tile, column block)
@@ -180,9 +182,16 @@ __device__ __forceinline__ LinF2 lin_phi(float x, float y) {
     return LinF2(x < 0.0f ? px : ux, y < 0.0f ? py : uy);
 }
 
-// N (even) values through the activation, in place, two at a time.  silu and the
-// gelus take the exponential and the quotient from the special function unit: a
-// few units in the last place of a factor at most 1.  NaN stays NaN.
+// N (even) values through the activation, in place, two at a time.  NaN stays NaN.
+// silu and the gelus take the exponential and the quotient from the special
+// function unit and the normal distribution from a polynomial, for binary32 Y
+// too: chosen for the pair kernel, whose epilogue shares the issue slots with the
+// conversion (M 4096, N = K = 8192 with gelu_tanh: 9 % less time than with expf and a
+// division, forms of its own for a residual and for none included).  Measured over
+// [-30, 30] against binary64, in 2^-24 max(|z|, 1): at most 2.8, 2.9 and 2.8 for silu, gelu and
+// gelu_tanh (torch's binary32 forms: 2.0 each).  In the negative tail silu is off by
+// 5e-7 of its value at -6 and by 2e-6 at -30, gelu_tanh by 3e-6 at -6, and gelu,
+// whose error is absolute, by 4e-3 at -6.
 template <int N>
 __device__ __forceinline__ void lin_act(float (&z)[N], int act) {
     // one test of `act` for all of them, and a loop of its own for each
@@ -336,7 +345,7 @@ __device__ __forceinline__ void lin_tmem_drain(uint32_t taddr, float (&v)[16][4]
 
 // v[a ..] = v[b ..], 16 values, as moves that stay where they are written: from
 // assignments the compiler makes copies of the whole array on every way through
-// the pair kernel's loop (8192 rows over 32 experts: 153 us for 146, 20 moves for
+// the pair kernel's loop (8192 rows over 32 experts: 5 % more time, 20 moves for
 // each element of Y).
 __device__ __forceinline__ void lin_move16(float (&v)[16][4], int a, int b) {
 #define GQ_OUT4(j) "=f"(v[a + j][0]), "=f"(v[a + j][1]), "=f"(v[a + j][2]), "=f"(v[a + j][3])
@@ -365,8 +374,7 @@ __device__ __forceinline__ float lin_ld_peer(uint32_t addr, uint32_t rank) {
 // g_mma_stage_ts, but from the low word of X's shared memory descriptor, and all
 // its arguments the same in every lane, so that the compiler can keep them in
 // uniform registers.  The issuing warp is the narrow place of a stage's way: with
-// descriptors put together anew for each column block M 16, N = K = 16384 takes
-// 43.7 us instead of 41.2.
+// descriptors put together anew for each column block M 16, N = K = 16384 takes 6 % more time.
 __device__ __forceinline__ uint32_t lin_desc_low(uint32_t addr) { return (uint32_t)g_smem_desc(addr); }
 template <int CTAS>
 __device__ __forceinline__ void lin_mma(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc,
@@ -607,8 +615,8 @@ struct LinShape {
     static constexpr uint32_t acc_cols = NT <= 64 ? 64 : NT;
     static constexpr uint32_t slots = (256 - acc_cols) / 64;             // stages of A in TMEM
     // Conversion groups of four warps, and how many of them share a stage.  Two whole-stage groups wait and hand over
-    // half as often as four half-stage ones (M 16, N = K = 16384: 47.6 us against 51.9); with 128 tokens the MMAs
-    // leave only two slots, and four groups hide more (M 4096, N = K = 8192: 595 us against 736).
+    // half as often as four half-stage ones (M 16, N = K = 16384: 8 % less time); with 128 tokens the MMAs
+    // leave only two slots, and four groups hide more (M 4096, N = K = 8192 in this kernel: 19 % less).
     static constexpr int groups = NT <= 64 ? 2 : 4, parts = NT <= 64 ? 1 : 2;
     static constexpr int threads = 64 + 128 * groups;
     static constexpr uint32_t bars = 8 * (2 * kLinMaxStages + 2 * 4 + 2) + 64;
@@ -833,8 +841,8 @@ __global__ void __launch_bounds__(LinShape<QB, NT>::threads, 2) linear_kernel(co
 // tokens, each between two stages of conversion, so that the MMAs never wait for
 // a whole epilogue.  Block 0's barriers gather both blocks' conversions (wready)
 // and drains (acc_empty); the MMAs' commits arrive on both blocks' barriers.
-// Bound: the tensor pipe.  M 4096, N = K = 8192, bias, gelu_tanh and residual: 363 us
-// (1515 TFLOP/s) on a cool device.
+// Bound: the tensor pipe.  M 4096, N = K = 8192, bias, gelu_tanh and residual: 368 us
+// (1495 TFLOP/s) on a cool device, 435 in a loop that the power cap holds at 1.33 GHz.
 constexpr int kPairNT = 256;
 constexpr int kPairThreads = 128 + 512;
 constexpr int kPairRoleRegs = 32, kPairConvRegs = 112;     // 4 * 32 + 16 * 112 = 20 * 96: what the block is launched with
@@ -856,7 +864,7 @@ struct PairShape {
 // in tensor memory (ordered by the tcgen05 fences) or came by a copy that the
 // arriving thread has waited for, so the default scope will do; a release at
 // cluster scope waits for the thread's earlier stores to reach the other SM
-// (M 4096, N = K = 8192: 381 us against 355).
+// (M 4096, N = K = 8192: 7 % more time).
 __device__ __forceinline__ void lin_arrive_lead(uint32_t bar) {
     asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
                  "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
@@ -1018,7 +1026,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 --left;
                 if (n < P.N && c < mv) {                   // (the residual is in L2: the copying warp asked for it)
                     // 16 rows at once, or eight with a residual, whose loads take as many registers: each form on its own
-                    // keeps within them (one for both: 399 us for 369, M 4096, N = K = 8192)
+                    // nearly keeps within them (56 bytes of reloads in all; one form for both: 8 % more time, M 4096,
+                    // N = K = 8192)
                     if (P.epi.residual) {
 #pragma unroll
                         for (int h = 0; h < 16; h += 8) {
