@@ -575,6 +575,8 @@ def _on_given(stream, index: int, y, fn, *args) -> torch.Tensor:
     is kept for the caller's own stream too, which is to use it."""
     if index < 0:
         raise ValueError("libgq takes CUDA tensors")
+    if _stream(stream) == torch._C._cuda_getCurrentRawStream(index):
+        return fn(*args)
     with torch.cuda.stream(_stream_of(stream, index)):
         out = fn(*args)
     if y is None:

@@ -91,6 +91,28 @@ def test_results_on_another_stream_keep_their_memory(gq):
     assert torch.equal(y, want)
 
 
+def test_every_way_to_name_a_stream(gq):
+    """The current stream, the default one by its handle 0, a torch stream, its handle, an object that holds one; the
+    current one a side stream too."""
+    class Holder:
+        def __init__(self, s):
+            self.cuda_stream = s.cuda_stream
+
+    rng = np.random.default_rng(29)
+    W = Weight(gq, rng, 1, 130, 192, 6)
+    x = _x(rng, 5, 192)
+    want = gq.gemm_epilogue(x, gq.tile_weight(W.packed[0], 192, 6), W.scale[0], 6)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for cur in (torch.cuda.default_stream(), other):
+        with torch.cuda.stream(cur):
+            for s in (None, 0, torch.cuda.current_stream(), side, side.cuda_stream, Holder(side), torch.cuda.default_stream()):
+                y = gq.gemm_epilogue(x, gq.tile_weight(W.packed[0], 192, 6, stream=s), W.scale[0], 6, stream=s,
+                                     check_status=True)
+                torch.cuda.synchronize()
+                assert torch.equal(y, want)
+
+
 def test_stream_refusals(gq):
     W = Weight(gq, np.random.default_rng(23), 1, 64, 64, 6)
     x = _x(np.random.default_rng(23), 3, 64)
