@@ -540,9 +540,10 @@ GQ_API gq_status gq_gemm_grouped(const void* d_x, int64_t M, int64_t K, int64_t 
  * at most about once in 10^5 steps.)
  *
  * States: binary32 m and v (state_bits 32), or 8 bits each with binary32
- * scales per block of 256 consecutive elements.  v is a fourth power, v = RN(RN(qv^2)^2 * sv),
- * qv uint8 (it spans nine decades of a block, the codes densest where the
- * block's large values lie); m, qm int8 in [-127, 127], is
+ * scales per block of 256 consecutive elements.  v is a fourth power,
+ *   v = RN(RN(qv^2)^2 * sv), qv uint8
+ * (it spans nine decades of a block, the codes densest where the block's large
+ * values lie); m, with qm int8 in [-127, 127], is
  *   m = RN(qm * sm)            linear codes (state_bits 8), or
  *   m = RN(qm * |qm| * sm)     square codes (GQ_ADAMW_8_SQUARE).
  * New codes, with a = max |m'| (max v') of the block and f(q) = RN((q^2)^2):
@@ -553,15 +554,18 @@ GQ_API gq_status gq_gemm_grouped(const void* d_x, int64_t M, int64_t K, int64_t 
  *   qv = q0 + (RN(u2 * RN(f(q0 + 1) - f(q0))) < RN(x - f(q0))), and 1 where that is 0 but x > 0;
  *   a < 2^-80 gives scale 0 and codes 0.
  * u1, u2 are 16 random bits each (k * 2^-16) from a hash of the element's
- * index, the tensor's place in the batch, the step and the seed: reproducible, and
- * m's mean and that of v above its first code are right to 2^-16 of a code's step, so that
- * changes of a state smaller than that step are not lost.  (v below its
- * first code is stored as that code, above its value, since the step divides by its root.)
+ * index, the tensor's place in the batch, the step and the seed: reproducible,
+ * and the mean of m, and that of v above its first code, is right to 2^-16 of
+ * a code's step, so that changes of a state smaller than that step are not
+ * lost.  (v below its first code is stored as that code, above its value, since
+ * the step divides by its root.)
  *
- * Which codes: an element far below its block's largest keeps v to a / 255^4 but, in linear codes, m only
- * as 0 or a whole a / 127, and then moves by many times lr in one step; square codes step as
- * sqrt(v) = qv^2 * sqrt(sv) does.  Largest |update| / lr (and root mean square) over 200 steps, b = (0.9, 0.95), gradients
- * N(0, 1) times a scale of each element's own; 32-bit states: 1.0 (0.26) throughout:
+ * Which codes: an element far below its block's largest keeps v to a / 255^4
+ * but, in linear codes, m only as 0 or a whole a / 127, and then moves by many
+ * times lr in one step; square codes step as sqrt(v) = qv^2 * sqrt(sv) does.
+ * Largest |update| / lr (and root mean square) over 200 steps, b = (0.9, 0.95),
+ * gradients N(0, 1) times a scale of each element's own; 32-bit states give 1.0
+ * (0.26) throughout:
  *   scales in a block          linear         square
  *   equal                      1.3 (0.26)     1.0 (0.26)
  *   exp(N(0, 1))               4.5 (0.27)     1.2 (0.26)
